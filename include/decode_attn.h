@@ -284,6 +284,64 @@ int decode_attn_static_scratch(const decode_attn_params* p, const void* q, const
                                const int32_t* seq_lens, void* out, int32_t* err_flag,
                                void* stream);
 
+/*
+ * ---- New tokens by the chunk ----
+ *
+ * A ragged batch: sequence b brings the rows [offsets[b], offsets[b + 1]) of
+ * the new tokens' tensors, n_b rows, at its last n_b positions, seq_lens[b] -
+ * n_b + i for the i-th.  offsets: [B + 1] int32 device, ascending, inside
+ * [0, total]; n_b may be 0.  Rows that no sequence owns are neither read for
+ * a result nor written.  Offsets that do not ascend or leave [0, total] raise
+ * DECODE_ATTN_DEV_BAD_LEN; the rows of such a sequence are left as they were.
+ */
+
+/*
+ * Attention of the new tokens over the paged 16-bit cache (prompt chunks,
+ * verification of several drafted tokens): token i of sequence b, at position
+ * p = seq_lens[b] - n_b + i, attends the positions k <= p (k > p - window with
+ * a window):
+ *   out[r][hq][:] = sum_k softmax_k(scale * q[r][hq] . k_k) * v_k.
+ * q, out: [total_queries][Hq][D]; pools, page table and seq_lens as for
+ * decode_attn, the new tokens' K/V rows already in the cache.  Of *p,
+ * num_queries, variant, split_min and schedule are not used; max_seq_len only
+ * steers the plan (any length up to the table's capacity gives its result);
+ * force_chunk > 0 sets the keys per shard.  No limit on the tokens per
+ * sequence.  Deterministic: the same bits every run.
+ * A token before position 0 (n_b > seq_lens[b]) or of a sequence with a
+ * length outside [0, capacity] (DECODE_ATTN_DEV_BAD_LEN) gets a zero row, and
+ * so does one that attends a page id outside [0, P)
+ * (DECODE_ATTN_DEV_BAD_PAGE; with a window, one whose range lies between two
+ * such pages of its tile may, too).  Positions that no token of the batch
+ * attends may hold anything.  A NaN or Inf in a V row that some token of the
+ * batch attends may also reach tokens of the same sequence before it.
+ * workspace: decode_attn_chunk_workspace_size() bytes, 256-byte aligned;
+ * scratch that needs no clearing, 0 bytes for a plan without shards.  It may
+ * be a workspace of decode_attn, whose shard tickets (its first 64 KiB) stay
+ * as they are.  Calls sharing one must not overlap on the GPU.  err_flag and
+ * alignment as for decode_attn.
+ */
+typedef struct decode_attn_chunk_plan {
+  int32_t tile_tokens;       /* tokens of one 128-row tile: floor(128 / G) */
+  int32_t item_tokens;       /* tokens of one CTA (two tiles; one at D = 256) */
+  int32_t slots;             /* tiles of item_tokens over all sequences, at most */
+  int32_t max_shards;        /* CTAs that share one tile's key range, at most */
+  int32_t shard_keys;        /* keys a shard is made for: shorter ranges take fewer shards */
+  int32_t grid;              /* CTAs: slots * max_shards * Hkv */
+  size_t workspace_bytes;    /* 64 KiB + (m, l) and fp32 accumulators per row and shard; or 0 */
+} decode_attn_chunk_plan;
+
+int decode_attn_chunk_make_plan(const decode_attn_params* p, int32_t total_queries,
+                                int32_t num_sms, decode_attn_chunk_plan* plan);
+
+/* Workspace bytes of decode_attn_chunk on `device`; 0 also for invalid arguments. */
+size_t decode_attn_chunk_workspace_size(const decode_attn_params* p, int32_t total_queries,
+                                        int device);
+
+int decode_attn_chunk(const decode_attn_params* p, int32_t total_queries, const void* q,
+                      const void* k_pages, const void* v_pages, const int32_t* page_table,
+                      const int32_t* query_offsets, const int32_t* seq_lens, void* out,
+                      void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ entry point without the built library raises.
 
 Entry points (same names as the C ABI):
   decode_attn, decode_attn_split, decode_attn_combine, decode_attn_host,
-  decode_attn_workspace_size, decode_attn_make_plan, decode_attn_strerror
+  decode_attn_workspace_size, decode_attn_make_plan, decode_attn_strerror;
+  decode_attn_chunk (attention of a ragged batch of new tokens)
 """
 from __future__ import annotations
 
@@ -29,6 +30,8 @@ __all__ = [
     "decode_attn_static_scratch", "decode_attn_workspace_clear", "DEV_WORKSPACE",
     "decode_kv_append", "decode_attn_append", "DTYPE_FP16", "DTYPE_BF16",
     "SCHEDULE_AUTO", "SCHEDULE_GRID", "SCHEDULE_CLUSTER",
+    "DecodeAttnChunkPlan", "decode_attn_chunk", "decode_attn_chunk_make_plan",
+    "decode_attn_chunk_workspace_size",
 ]
 
 VARIANT_AUTO, VARIANT_SIMT, VARIANT_MMA = 0, 1, 2
@@ -63,6 +66,15 @@ class DecodeAttnPlan(ctypes.Structure):
         "split", "variant", "group_pad", "tile_tokens", "chunk_tokens", "max_shards",
         "grid_x", "grid_y", "grid_z", "ctas_per_sm", "head_fastest", "ring_stages",
         "cluster", "balanced")] + [
+        ("workspace_bytes", ctypes.c_size_t)]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class DecodeAttnChunkPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "tile_tokens", "item_tokens", "slots", "max_shards", "shard_keys", "grid")] + [
         ("workspace_bytes", ctypes.c_size_t)]
 
     def as_dict(self):
@@ -110,6 +122,13 @@ def load_library():
             lib.decode_attn_append.restype = ctypes.c_int
             lib.decode_attn_workspace_clear.argtypes = [PP, P, sz, P]
             lib.decode_attn_workspace_clear.restype = ctypes.c_int
+            lib.decode_attn_chunk_make_plan.argtypes = [PP, i32, i32,
+                                                        ctypes.POINTER(DecodeAttnChunkPlan)]
+            lib.decode_attn_chunk_make_plan.restype = ctypes.c_int
+            lib.decode_attn_chunk_workspace_size.argtypes = [PP, i32, ctypes.c_int]
+            lib.decode_attn_chunk_workspace_size.restype = sz
+            lib.decode_attn_chunk.argtypes = [PP, i32, P, P, P, P, P, P, P, P, sz, P, P]
+            lib.decode_attn_chunk.restype = ctypes.c_int
             lib.decode_attn_strerror.argtypes = [ctypes.c_int]
             lib.decode_attn_strerror.restype = ctypes.c_char_p
             _lib = lib
@@ -449,4 +468,117 @@ def decode_attn_static_scratch(q, k_pages, v_pages, page_table, seq_lens, scale:
                               _stream_handle(stream))
     if st:
         raise DecodeAttnError(st, "decode_attn_static_scratch")
+    return out
+
+
+# ------------------------------------------------ new tokens by the chunk
+
+def _scratch(device, nbytes: int, zero: bool, stream=None):
+    """A workspace for one call of the entry points below: cached per
+    (device, stream) like decode_attn's, but a call under stream capture gets
+    one of its own, so that two captured graphs never share one."""
+    import torch
+    if nbytes == 0:
+        return None
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    s = stream if stream is not None else torch.cuda.current_stream(index)
+    with torch.cuda.stream(s):
+        capturing = torch.cuda.is_current_stream_capturing()
+        key = (index, s.cuda_stream, zero)
+        buf = None if capturing else _ws_cache.get(key)
+        if buf is None or buf.numel() < nbytes:
+            make = torch.zeros if zero else torch.empty
+            buf = make(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            if not capturing:
+                _ws_cache[key] = buf
+    return buf
+
+
+def _check_offsets(t, batch: int, name: str, device):
+    import torch
+    _check(t, torch.int32, name, device)
+    if tuple(t.shape) != (batch + 1,):
+        raise ValueError(f"{name} must be [B + 1] = [{batch + 1}], got {list(t.shape)}")
+
+
+def _check_table(page_table, seq_lens, device):
+    import torch
+    _check(page_table, torch.int32, "page_table", device)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    if seq_lens is not None:
+        _check(seq_lens, torch.int32, "seq_lens", device)
+        if tuple(seq_lens.shape) != (page_table.shape[0],):
+            raise ValueError(f"seq_lens must be [B] = [{page_table.shape[0]}]")
+
+
+def _check_err_flag(err_flag, device):
+    import torch
+    if err_flag is not None:
+        _check(err_flag, torch.int32, "err_flag", device)
+
+
+def decode_attn_chunk_make_plan(params: DecodeAttnParams, total_queries: int,
+                                num_sms: int) -> DecodeAttnChunkPlan:
+    plan = DecodeAttnChunkPlan()
+    st = load_library().decode_attn_chunk_make_plan(ctypes.byref(params), int(total_queries),
+                                                    int(num_sms), ctypes.byref(plan))
+    if st:
+        raise DecodeAttnError(st, "decode_attn_chunk_make_plan")
+    return plan
+
+
+def decode_attn_chunk_workspace_size(params: DecodeAttnParams, total_queries: int,
+                                     device: int) -> int:
+    return int(load_library().decode_attn_chunk_workspace_size(
+        ctypes.byref(params), int(total_queries), int(device)))
+
+
+@_on_device_of("q", 0)
+def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, scale: float,
+                      window: int = 0, out=None, max_seq_len: Optional[int] = None,
+                      workspace=None, err_flag=None, force_chunk: int = 0, stream=None):
+    """Attention of a ragged batch of new tokens over the paged cache.
+
+    q [total, Hq, D] fp16 or bf16: sequence b owns the rows query_offsets[b]
+    to query_offsets[b + 1] (int32 [B + 1]) and they sit at its last
+    positions; seq_lens [B] counts them, and their K/V rows are in the cache
+    already.  Token at position p attends the positions up to p, the last
+    ``window`` of them with a window.  Returns ``out`` like q; rows that no
+    sequence owns keep what they held (a new ``out`` is not initialised).
+    ``max_seq_len`` (a host-side bound) only steers the plan."""
+    import torch
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("decode_attn_chunk runs on CUDA tensors")
+    et = _elem_dtype(q)
+    _check(q, et, "q", dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [total, Hq, D]")
+    _check(k_pages, et, "k_pages", dev)
+    _check(v_pages, et, "v_pages", dev)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [P, PS, Hkv, D], both of one shape")
+    _check_table(page_table, seq_lens, dev)
+    _check_offsets(query_offsets, page_table.shape[0], "query_offsets", dev)
+    _check_err_flag(err_flag, dev)
+    total, B = q.shape[0], page_table.shape[0]
+    p = make_params(q, k_pages, page_table, scale, window, max_seq_len, 0, 0, force_chunk)
+    p.batch, p.num_queries = B, 1
+    if out is None:
+        out = torch.empty_like(q)
+    _check(out, et, "out", dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = _scratch(dev, decode_attn_chunk_workspace_size(
+            p, total, dev.index if dev.index is not None else torch.cuda.current_device()),
+            False, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load_library().decode_attn_chunk(
+        ctypes.byref(p), total, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+        _ptr(query_offsets), _ptr(seq_lens), _ptr(out), _ptr(workspace), ws_bytes,
+        _ptr(err_flag), _stream_handle(stream))
+    if st:
+        raise DecodeAttnError(st, "decode_attn_chunk")
     return out

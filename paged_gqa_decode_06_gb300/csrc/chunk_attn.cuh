@@ -1,0 +1,591 @@
+// Attention of a chunk of new tokens over the paged cache: a ragged batch of
+// query tokens (sequence b brings n_b of them, the last n_b of its L_b
+// positions), causal, grouped-query, with an optional sliding window:
+//   out[t] = sum_k softmax_k(scale * q_t . k) v_k,  k in (p_t - window, p_t].
+//
+// One CTA owns (tiles of query rows, KV head h, shard of the key range).  The
+// G query heads of the group are packed with the tokens into the 128 rows of
+// a matrix-instruction tile (row = token * G + g, floor(128 / G) tokens), so
+// a K/V row read serves every head of the group and a short chunk still fills
+// the tile.  Two such tiles (streams) share every K/V tile at head_dim <= 128;
+// at 256 the accumulator of one fills half of the tensor memory.
+//
+// Both products run on tcgen05: S = Q . K^T from shared memory into tensor
+// memory, and O += P . V with P read from tensor memory, where the softmax
+// threads write it over S.  Roles: a producer warp (TMA through the page
+// table), a warp that issues the matrix instructions, and 128 threads per
+// stream that keep one row each (running maximum, sum).  The issue order is
+//   S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
+// over units u = (key tile, stream): while the softmax of one unit runs, the
+// products of the other stream do, so each hides the other.
+//
+// Both K and V tiles lie in shared memory as [group of 8 tokens][D / 64][8
+// tokens][64 dims] with the 128-byte swizzle: one TMA box brings a page's
+// piece with all its dims (a 5-D view of the pool), and the groups are evenly
+// spaced whatever the page size, which is what an operand descriptor wants:
+// K as K-major with D * 16 bytes between groups of 8 tokens, V as MN-major
+// with 1024 bytes between chunks of 64 dims.
+//
+// P is rounded once to the element type for the second product (the weights
+// of a row are at most 2^8 and the largest is at least 1, so each keeps that
+// type's relative precision); sums, maxima and accumulators are fp32.
+#pragma once
+
+#include <type_traits>
+
+#include "combine.cuh"  // grid_dependency_wait, grid_launch_dependents
+#include "elem.cuh"
+#include "ragged.cuh"
+#include "tcgen05.cuh"
+
+namespace pgd {
+
+struct ChunkArgs {
+  const int32_t* page_table;  // [B][max_pages]
+  const int32_t* offsets;     // [B + 1] rows of each sequence
+  const int32_t* seq_lens;    // [B]
+  void* out;                  // [total][Hq][D]
+  float* ws_acc;              // [total * Hq][max_shards][D]   (split plans)
+  float2* ws_ml;              // [total * Hq][max_shards]; l = -1 marks a bad row
+  int32_t* err;               // nullable
+  int32_t B, total, Hq, Hkv, G;
+  int32_t max_pages, num_pages, page_size, page_shift, box_t;
+  int32_t window;
+  int32_t tile_tok;           // tokens of one stream's 128 rows
+  int32_t item_tok;           // tokens of one CTA (all streams)
+  int32_t slots;              // tiles of item_tok tokens over all sequences, at most
+  int32_t max_shards, shard_tiles;
+  int32_t stall_tx;           // 0; a test sets extra bytes on the first K tile's barrier
+  float scale_log2;
+};
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int kStreams = D <= 128 ? 2 : 1;
+  static constexpr int kKeys = D <= 128 ? 128 : 64;  // keys of one tile
+  static constexpr int kThreads = kStreams * 128 + 128;
+  static constexpr int kTileBytes = kKeys * D * 2;
+  static constexpr int kQBytes = 128 * D * 2;  // one stream
+  // the ring holds K and V tiles in turn
+  static constexpr int kRing = D == 64 ? 8 : 5;
+  static constexpr int kSmemBytes = kStreams * kQBytes + kRing * kTileBytes + 1024;
+  static constexpr uint32_t kTmemCols = 512;
+};
+
+// One CTA's share of the work, found from its slot.
+struct ChunkItem {
+  int32_t b, t0, t1;     // sequence, its query tokens [t0, t1)
+  int32_t row0;          // row of t0 among all tokens
+  int32_t p0;            // position of t0
+  int32_t lo, hi;        // keys that some query of the item attends
+  int32_t base, tiles;   // first key of the first tile, number of key tiles
+  int32_t shards;        // CTAs that share the tiles (0: nothing to attend)
+  int32_t status;
+  bool any;              // the slot holds query tokens
+};
+
+// Sequence b owns the slots [offsets[b] / item_tok + b, offsets[b+1] /
+// item_tok + b + 1): at least the tiles it needs, and an ascending function
+// of b, so a slot finds its sequence by search.
+template <int KT>
+__device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, int lane) {
+  ChunkItem it{};
+  auto first_slot = [&](int b) { return (int64_t)(a.offsets[b] / a.item_tok) + b; };
+  const int b = warp_search(a.B, slot, lane, first_slot);
+  if (b < 0) return it;
+  const RowRange r = row_range(a.offsets, b, a.total);
+  it.b = b;
+  if (!r.ok) {
+    it.status = DECODE_ATTN_DEV_BAD_LEN;
+    return it;
+  }
+  const int64_t t0 = ((int64_t)slot - (r.first / a.item_tok + b)) * a.item_tok;
+  if (t0 < 0 || t0 >= r.count) return it;
+  it.any = true;
+  it.t0 = (int32_t)t0;
+  it.t1 = min(r.count, it.t0 + a.item_tok);
+  it.row0 = r.first + it.t0;
+  const int32_t L = ld_global_s32(a.seq_lens + b);
+  if (L < 0 || L > a.max_pages * a.page_size) {
+    it.status = DECODE_ATTN_DEV_BAD_LEN;
+    return it;
+  }
+  it.p0 = L - r.count + it.t0;
+  it.hi = max(0, it.p0 + (it.t1 - it.t0));
+  it.lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
+  it.base = it.lo & ~(KT - 1);
+  it.tiles = it.hi > it.lo ? (it.hi - it.base + KT - 1) / KT : 0;
+  it.shards = min(a.max_shards, (it.tiles + a.shard_tiles - 1) / a.shard_tiles);
+  return it;
+}
+
+template <int D>
+__device__ __forceinline__ uint64_t k_desc(uint32_t tile) {
+  return tc_desc(tile, 16, D * 16);
+}
+template <int D>
+__device__ __forceinline__ uint64_t v_desc(uint32_t tile) {
+  return tc_desc(tile, 1024, D * 16);
+}
+
+template <int D, class E>
+__global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                      const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const ChunkArgs a) {
+  using C = ChunkCfg<D>;
+  constexpr int NS = C::kStreams, KT = C::kKeys, NR = C::kRing;
+  constexpr int kProducer = NS * 4, kMma = NS * 4 + 1;  // warps
+  constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
+  constexpr uint32_t kIdescS = tc_idesc(128, KT, kBf16, false);
+  constexpr uint32_t kIdescO = tc_idesc(128, D, kBf16, true);
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t q_full, full_bar[NR], empty_bar[NR];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[NS];
+  __shared__ uint32_t tmem_s;
+  __shared__ volatile int32_t abort_s;
+  __shared__ int32_t bad_lo_s, bad_hi_s;  // positions in pages outside the pool
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* ring = smem + NS * C::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == kProducer * 32) {
+    prefetch_tensormap(&tmap_q);
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+    mbar_init(smem_u32(&q_full), 1);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(smem_u32(&full_bar[i]), 1);
+      mbar_init(smem_u32(&empty_bar[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 4);
+    }
+    for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&o_full[i]), 1);
+    fence_mbar_init();
+    abort_s = 0;
+    bad_lo_s = INT32_MAX;
+    bad_hi_s = -1;
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  const int h = blockIdx.x % a.Hkv;
+  const int shard = (blockIdx.x / a.Hkv) % a.max_shards;
+  // the last tiles of a sequence see the most keys: they start first
+  const int slot = a.slots - 1 - blockIdx.x / (a.Hkv * a.max_shards);
+  const ChunkItem it = chunk_item<KT>(a, slot, lane);
+  if (blockIdx.x == 0)  // offsets that no slot may lead to are checked once
+    for (int b = threadIdx.x; b < a.B; b += C::kThreads)
+      if (!row_range(a.offsets, b, a.total).ok) raise_error(a.err, DECODE_ATTN_DEV_BAD_LEN);
+  if (it.status != 0 && threadIdx.x == 0) raise_error(a.err, it.status);
+  if (!it.any) return;
+  if (it.shards == 0) {  // no key: zero rows
+    if (shard == 0) {
+      uint4* out = reinterpret_cast<uint4*>(a.out);
+      const int chunks = a.G * D / 8;
+      for (int e = threadIdx.x; e < (it.t1 - it.t0) * chunks; e += C::kThreads) {
+        const size_t at = ((size_t)(it.row0 + e / chunks) * a.Hq + (size_t)h * a.G) * (D / 8) +
+                          e % chunks;
+        if (PGD_IN(at, (size_t)a.total * a.Hq * (D / 8), a.err)) out[at] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  if (shard >= it.shards) return;
+  const int tile0 = (int)((int64_t)it.tiles * shard / it.shards);
+  const int ntiles = (int)((int64_t)it.tiles * (shard + 1) / it.shards) - tile0;
+  const int key0 = it.base + tile0 * KT;  // first key of this CTA's first tile
+  const int ns = (it.t1 - it.t0) > a.tile_tok ? NS : 1;  // streams with tokens
+  const int units = ntiles * ns;
+
+  // two streams: 384 threads launched with 168 registers each; the row
+  // threads (a row of 128 scores apiece) take 224, the last warpgroup 56
+  constexpr int kOthers = NS * 128 + 32;  // the row threads and the issuing warp
+  if (warp >= kProducer) {
+    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kProducer) {
+      if (lane == 0) {
+        const uint32_t qb = smem_u32(&q_full);
+        mbar_arrive_expect_tx(qb, (uint32_t)(ns * (D / 64) * a.tile_tok * a.G * 128));
+        for (int s = 0; s < ns; ++s)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem_u32(smem + s * C::kQBytes + c * (128 * 128)), &tmap_q, 0, h * a.G,
+                        it.row0 + s * a.tile_tok, c, qb);
+      }
+      __syncwarp();
+      const int pieces = KT / a.box_t;
+      const int pool_groups = a.num_pages * (a.page_size / 8);
+      int issued = 0;
+      int coord = 0;
+      for (int r = 0; r < 2 * ntiles; ++r) {
+        const int slot_r = r % NR;
+        if ((r & 1) == 0 && lane < pieces) {
+          // this lane's piece of the tile: a row group of the pool, or one past
+          // it (zeros) where no query attends
+          const int ptok = key0 + (r >> 1) * KT + lane * a.box_t;
+          coord = pool_groups;
+          if (ptok < it.hi && ptok + a.box_t > it.lo) {
+            const size_t pi = (size_t)it.b * a.max_pages + (ptok >> a.page_shift);
+            const int phys = PGD_IN(pi, (size_t)a.B * a.max_pages, a.err) ? a.page_table[pi] : -1;
+            if (phys < 0 || phys >= a.num_pages) {
+              raise_error(a.err, DECODE_ATTN_DEV_BAD_PAGE);
+              atomicMin(&bad_lo_s, ptok);
+              atomicMax(&bad_hi_s, ptok + a.box_t);
+            } else {
+              coord = (phys << (a.page_shift - 3)) + ((ptok & (a.page_size - 1)) >> 3);
+            }
+          }
+        }
+        __syncwarp();
+        if (r >= NR) {
+          int go = 1;
+          if (lane == 0) {
+            if (!mbar_wait(smem_u32(&empty_bar[slot_r]), ((r / NR) & 1) ^ 1)) {
+              abort_s = 1;
+              raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+            }
+            go = abort_s ? 0 : 1;
+          }
+          if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        }
+        const uint32_t fb = smem_u32(&full_bar[slot_r]);
+        if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes + (r == 0 ? a.stall_tx : 0));
+        __syncwarp();
+        if (lane < pieces)
+          tma_load_5d(smem_u32(ring + slot_r * C::kTileBytes + lane * a.box_t * D * 2),
+                      (r & 1) ? &tmap_v : &tmap_k, 0, 0, 0, coord, h, fb);
+        issued = r + 1;
+      }
+      // this CTA's copies in flight have landed before the warp exits
+      if (lane == 0) {
+        mbar_wait(smem_u32(&q_full), 0);
+        for (int r = max(0, issued - NR); r < issued; ++r)
+          mbar_wait(smem_u32(&full_bar[r % NR]), (r / NR) & 1);
+      }
+      return;
+    }
+
+    if (warp == kMma) {
+      tmem_alloc(smem_u32(&tmem_s), C::kTmemCols);
+      tc_fence_before();
+      named_barrier_sync(1, kOthers);
+      tc_fence_after();
+      const uint32_t tmem = tmem_s, tmem_o = tmem + 2 * KT;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        if (ok && !mbar_wait(smem_u32(bar), parity)) {
+          abort_s = 1;
+          raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+        }
+        ok = __all_sync(0xffffffffu, ok && !abort_s);
+      };
+      auto issue_s = [&](int u) {  // S(u) = Q . K^T
+        const int j = u / ns, s = u % ns, r = 2 * j;
+        if (s == 0) wait(&full_bar[r % NR], (r / NR) & 1);
+        if (!ok) return;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t qd = tc_desc(smem_u32(smem + s * C::kQBytes), 16, 1024);
+          const uint64_t kd = k_desc<D>(smem_u32(ring + (r % NR) * C::kTileBytes));
+  #pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int c = ks >> 2, in = (ks & 3) * 2;  // 32 bytes inside a 64-dim chunk
+            tc_mma_ss(tmem + (u & 1) * KT, qd + c * (128 * 128 / 16) + in, kd + c * (1024 / 16) + in,
+                      kIdescS, ks > 0);
+          }
+          tc_commit(smem_u32(&s_full[u & 1]));
+          if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
+        }
+        __syncwarp();
+      };
+      wait(&q_full, 0);
+      issue_s(0);
+      if (units > 1) issue_s(1);
+      for (int u = 0; u < units && ok; ++u) {
+        const int j = u / ns, s = u % ns, r = 2 * j + 1;
+        uint8_t* vt = ring + (r % NR) * C::kTileBytes;
+        if (s == 0) {
+          wait(&full_bar[r % NR], (r / NR) & 1);
+          // V rows of the tile outside the attended range (a page's other
+          // positions) become zeros: a zero weight must not meet a NaN
+          const int k0 = key0 + j * KT;
+          if (ok && (k0 < it.lo || k0 + KT > it.hi)) {
+            for (int e = lane; e < KT * (D / 8); e += 32) {
+              const int t = e / (D / 8), c = e % (D / 8);
+              if (k0 + t < it.lo || k0 + t >= it.hi)
+                *reinterpret_cast<uint4*>(vt + (t >> 3) * (D * 16) + (c >> 3) * 1024 +
+                                          (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+        }
+        wait(&p_full[u & 1], (u >> 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t vd = v_desc<D>(smem_u32(vt));
+  #pragma unroll
+          for (int ks = 0; ks < KT / 16; ++ks)  // O += P . V
+            tc_mma_ts(tmem_o + s * D, tmem + (u & 1) * KT + ks * 8, vd + ks * (D * 32 / 16), kIdescO,
+                      j > 0 || ks > 0);
+          tc_commit(smem_u32(&o_full[s]));
+          if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
+        }
+        __syncwarp();
+        if (u + 2 < units) issue_s(u + 2);
+      }
+      named_barrier_sync(1, kOthers);  // every row has been read out
+      tc_fence_after();
+      tmem_free(tmem, C::kTmemCols);
+    }
+    return;  // (two more warps only fill the warpgroup)
+  }
+
+  // ---------------------------------------------------------- softmax rows
+  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  named_barrier_sync(1, kOthers);  // the tensor memory is there
+  tc_fence_after();
+  const uint32_t tmem = tmem_s, tmem_o = tmem + 2 * KT;  // O after the two S buffers
+  const int s = warp >> 2;
+  if (s < ns) {
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int tok = row / a.G, g = row % a.G;
+    const int ts = it.t0 + s * a.tile_tok;                 // first token of the stream
+    const int te = min(it.t1, ts + a.tile_tok);            // one past its last
+    const bool live = tok < a.tile_tok && ts + tok < te;
+    const int pos = it.p0 + s * a.tile_tok + tok;          // this row's position
+    const int first_pos = it.p0 + s * a.tile_tok, last_pos = it.p0 + (te - it.t0) - 1;
+    const bool neg = a.scale_log2 < 0.f;
+    float m = -INFINITY;
+    uint64_t l2 = 0;  // two partial sums
+    bool ok = true;
+    for (int j = 0; j < ntiles; ++j) {
+      const int u = j * ns + s, buf = u & 1;
+      const uint32_t tm_s = tmem + buf * KT + lanes;
+      if (!mbar_wait(smem_u32(&s_full[buf]), (u >> 1) & 1)) {
+        abort_s = 1;
+        raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+      }
+      ok = __all_sync(0xffffffffu, !abort_s);
+      if (!ok) break;
+      tc_fence_after();
+      float x[KT];
+#pragma unroll
+      for (int c = 0; c < KT; c += 32) tmem_ld32(x + c, tm_s + c);
+      tmem_wait_ld();
+      const int k0 = key0 + j * KT;
+      float mult = fabsf(a.scale_log2);
+      if (neg)
+#pragma unroll
+        for (int i = 0; i < KT; ++i) x[i] = -x[i];
+      if (k0 + KT - 1 > first_pos || (a.window > 0 && k0 <= last_pos - a.window)) {
+        // the edge of some row's range crosses the tile; scaled before the
+        // mask, so that a scale of 0 leaves the mask standing
+        const int top = pos - k0;
+        const int bottom = a.window > 0 ? pos - a.window - k0 : -1;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) x[i] = (i <= top && i > bottom) ? x[i] * mult : -INFINITY;
+        mult = 1.f;
+      }
+      float mx0 = max3(x[0], x[1], x[2]), mx1 = x[3];
+#pragma unroll
+      for (int i = 4; i < KT; i += 4) {
+        mx0 = max3(mx0, x[i], x[i + 1]);
+        mx1 = max3(mx1, x[i + 2], x[i + 3]);
+      }
+      const float mx = fmaxf(mx0, mx1) * mult;
+      // The reference maximum follows only when it would grow by more than
+      // 2^8: the weights stay below that, and the accumulator is rescaled
+      // for a few tiles instead of nearly every one.
+      float alpha = 1.f;
+      if (mx > m + 8.f) {
+        alpha = fast_exp2(m - mx);
+        m = mx;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O holds the products up to the unit before: rescale it in place
+        if (!mbar_wait(smem_u32(&o_full[s]), (j - 1) & 1)) {
+          abort_s = 1;
+          raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+        }
+        if (!__all_sync(0xffffffffu, !abort_s)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t al = pair(alpha, alpha);
+        l2 = mul2(l2, al);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(o, tmem_o + s * D + lanes + c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          tmem_st32(tmem_o + s * D + lanes + c, reinterpret_cast<const uint32_t*>(o));
+        }
+      }
+      const float mu = m == -INFINITY ? 0.f : m;  // a row without a key so far
+      const uint64_t mult2 = pair(mult, mult), nm2 = pair(-mu, -mu);
+#pragma unroll
+      for (int c = 0; c < KT; c += 64) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 e = unpair(fma2(pair(x[c + 2 * i], x[c + 2 * i + 1]), mult2, nm2));
+          const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
+          l2 = add2(l2, pair(p0, p1));
+          w[i] = ElemOps<E>::pack2(p0, p1);
+        }
+        tmem_st32(tm_s + c / 2, w);
+      }
+      tmem_wait_st();
+      // A parity tells only two neighbouring phases apart: before the last
+      // weights go out, the product before theirs is known to be done (it is,
+      // but for a single stream's), so that the wait below means the last one.
+      if (j == ntiles - 1 && j > 0 && !mbar_wait(smem_u32(&o_full[s]), (j - 1) & 1)) {
+        abort_s = 1;
+        raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+    }
+    if (ok && !mbar_wait(smem_u32(&o_full[s]), (ntiles - 1) & 1)) {
+      abort_s = 1;
+      raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+    }
+    ok = __all_sync(0xffffffffu, !abort_s);
+    tc_fence_after();
+    const float2 lh = unpair(l2);
+    const float l = lh.x + lh.y;
+    // rows that attend a page outside the pool are zeroed
+    const bool dead = !ok || (pos >= bad_lo_s && (a.window <= 0 || pos - a.window + 1 < bad_hi_s));
+    const size_t orow = (size_t)(it.row0 + s * a.tile_tok + tok) * a.Hq + (size_t)h * a.G + g;
+    const bool in = live && PGD_IN(orow, (size_t)a.total * a.Hq, a.err);
+    if (it.shards == 1) {
+      const float inv = dead || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D);
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (ok) tmem_ld32(o, tmem_o + s * D + lanes + c);
+        tmem_wait_ld();
+        if (!in) continue;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dst[c / 8 + i] = make_uint4(ElemOps<E>::pack2(o[8 * i], o[8 * i + 1]),
+                                      ElemOps<E>::pack2(o[8 * i + 2], o[8 * i + 3]),
+                                      ElemOps<E>::pack2(o[8 * i + 4], o[8 * i + 5]),
+                                      ElemOps<E>::pack2(o[8 * i + 6], o[8 * i + 7]));
+      }
+    } else {
+      const size_t slot_w = orow * a.max_shards + shard;
+      float4* dst = reinterpret_cast<float4*>(a.ws_acc + slot_w * D);
+      if (in) a.ws_ml[slot_w] = make_float2(m, dead ? -1.f : l);
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (ok) tmem_ld32(o, tmem_o + s * D + lanes + c);
+        tmem_wait_ld();
+        if (!in || dead) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  named_barrier_sync(1, kOthers);
+}
+
+// Merges the shards' partials of every row of a split plan, in ascending
+// shard order (same bits every run): one warp per row, launched as a
+// programmatic dependent of the attention kernel.
+constexpr int kChunkCombineRows = 8;
+
+template <int D, class E>
+__global__ void __launch_bounds__(kChunkCombineRows * 32)
+    chunk_combine_kernel(const ChunkArgs a) {
+  constexpr int KT = ChunkCfg<D>::kKeys;
+  constexpr int V = D / 32;  // dims per lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = a.item_tok * a.G;
+  const int blocks = (rows + kChunkCombineRows - 1) / kChunkCombineRows;
+  const int h = (blockIdx.x / blocks) % a.Hkv;
+  const int slot = blockIdx.x / (blocks * a.Hkv);
+  const int r = (blockIdx.x % blocks) * kChunkCombineRows + warp;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const ChunkItem it = chunk_item<KT>(a, slot, lane);
+  const int tok = r / a.G, g = r % a.G;
+  if (!it.any || it.shards < 2 || r >= rows || it.t0 + tok >= it.t1) return;
+  const size_t row = (size_t)(it.row0 + tok) * a.Hq + (size_t)h * a.G + g;
+  if (!PGD_IN(row, (size_t)a.total * a.Hq, a.err)) return;
+  const float2* ml = a.ws_ml + row * a.max_shards;
+  const float* acc = a.ws_acc + row * a.max_shards * D + lane * V;
+  float M = -INFINITY;
+  bool dead = false;
+  for (int s0 = 0; s0 < it.shards; s0 += 32) {
+    const float2 v = s0 + lane < it.shards ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, v.x);
+    dead |= v.y < 0.f;
+  }
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+  dead = __any_sync(0xffffffffu, dead);
+  float o[V], L = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  if (!dead && M != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < it.shards; ++s) {
+      const float2 v = __ldcg(ml + s);
+      const float c = fast_exp2(v.x - M);
+      float x[V];
+      if constexpr (V == 2) {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(acc + (size_t)s * D));
+        x[0] = f.x;
+        x[1] = f.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(acc + (size_t)s * D + i));
+          x[i] = f.x;
+          x[i + 1] = f.y;
+          x[i + 2] = f.z;
+          x[i + 3] = f.w;
+        }
+      }
+      L = __fmaf_rn(c, v.y, L);
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = __fmaf_rn(c, x[i], o[i]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i)
+    w[i] = inv == 0.f ? 0u : ElemOps<E>::pack2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + lane * V);
+  if constexpr (V == 2) {
+    dst[0] = w[0];
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+}  // namespace pgd
