@@ -311,9 +311,9 @@ int decode_attn_static_scratch(const decode_attn_params* p, const void* q, const
  * length outside [0, capacity] (DECODE_ATTN_DEV_BAD_LEN) gets a zero row, and
  * so does one that attends a page id outside [0, P)
  * (DECODE_ATTN_DEV_BAD_PAGE; with a window, one whose range lies between two
- * such pages of its tile may, too).  Positions that no token of the batch
- * attends may hold anything.  A NaN or Inf in a V row that some token of the
- * batch attends may also reach tokens of the same sequence before it.
+ * such pages of its tile may, too).  What a token does not attend
+ * (later positions, positions before its window, a page's unused ones) never
+ * reaches its row, whatever it holds.
  * workspace: decode_attn_chunk_workspace_size() bytes, 256-byte aligned;
  * scratch that needs no clearing, 0 bytes for a plan without shards.  It may
  * be a workspace of decode_attn, whose shard tickets (its first 64 KiB) stay
@@ -341,6 +341,74 @@ int decode_attn_chunk(const decode_attn_params* p, int32_t total_queries, const 
                       const void* k_pages, const void* v_pages, const int32_t* page_table,
                       const int32_t* query_offsets, const int32_t* seq_lens, void* out,
                       void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
+
+/* Cell formats of the pools below. */
+#define DECODE_ATTN_KV_16BIT 0  /* 16-bit elements (params.dtype), no scales */
+#define DECODE_ATTN_KV_E4M3 1   /* 8-bit e4m3 codes [P][PS][Hkv][D] with fp32 scales
+                                   [P][Hkv][PS], one per (position, KV head) row of K and
+                                   of V: value = code * scale.  Any scale may be stored;
+                                   decode_kv_append_chunk writes powers of two. */
+
+/*
+ * Writes the new tokens' K/V rows into their pages: row i of sequence b (rows
+ * as above) goes to position seq_lens[b] - n_b + i.  k_new, v_new:
+ * [total_rows][Hkv][D] 16-bit.  DECODE_ATTN_KV_16BIT copies bit for bit
+ * (k_scales, v_scales unused, may be NULL).  DECODE_ATTN_KV_E4M3 quantises:
+ * per row and head the scale is the least power of two with max |x| <= 448 *
+ * scale, the code the nearest e4m3 number to x / scale (ties to even); a row
+ * whose largest magnitude is below 2^-100 becomes zeros with scale 0.  A NaN
+ * becomes a NaN code; an Inf takes its row's scale to 2^120 and reads back as
+ * Inf, the row's finite values as 0.
+ * A row before position 0 (n_b > seq_lens[b]) is not written; a position past
+ * the table or a negative length raises DECODE_ATTN_DEV_BAD_LEN, a page id
+ * outside [0, P) DECODE_ATTN_DEV_BAD_PAGE, and such a row is not written.
+ * Two rows that name the same cell leave either's.  Uses batch, num_kv_heads,
+ * head_dim, page_size, max_pages_per_seq, num_pages and dtype of *p (the
+ * other fields must still be valid).  Pointers 16-byte aligned.
+ */
+int decode_kv_append_chunk(const decode_attn_params* p, int32_t kv_format, int32_t total_rows,
+                           const void* k_new, const void* v_new, const int32_t* row_offsets,
+                           const int32_t* seq_lens, void* k_pages, void* v_pages,
+                           float* k_scales, float* v_scales, const int32_t* page_table,
+                           int32_t* err_flag, void* stream);
+
+/*
+ * Reads rows of the cache back: output row r of sequence b (row_offsets as
+ * above) is position starts[b] + r - row_offsets[b] (starts NULL: 0), as
+ * 16-bit elements [total_rows][Hkv][D]: a bit-for-bit copy, or code * scale
+ * rounded once.  With offsets that are multiples of a page size the outputs
+ * are a paged 16-bit pool in their own right (pages in order), which
+ * decode_attn_chunk takes.  A position outside the table
+ * (DECODE_ATTN_DEV_BAD_LEN) or in a page outside [0, P)
+ * (DECODE_ATTN_DEV_BAD_PAGE) gives a zero row; rows that no sequence owns are
+ * left as they were.
+ */
+int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total_rows,
+                   const void* k_pages, const void* v_pages, const float* k_scales,
+                   const float* v_scales, const int32_t* page_table, const int32_t* row_offsets,
+                   const int32_t* starts, void* k_out, void* v_out, int32_t* err_flag,
+                   void* stream);
+
+/*
+ * One decode step over an 8-bit cache: decode_attn's operation (its layouts
+ * of q, out, page table and lengths, windows, num_queries with T * G <= 16,
+ * error bits and zero rows, schedules GRID and CLUSTER, split_min and
+ * force_chunk) with k_t = code * scale, likewise v_t, of a
+ * DECODE_ATTN_KV_E4M3 pool.  q and out are params.dtype.  The plan is that of
+ * decode_attn_quant_make_plan; variant must be AUTO or MMA.
+ * workspace: decode_attn_quant_workspace_size() bytes, with decode_attn's
+ * rules (tickets zero on entry, left zero); one zeroed buffer serves both.
+ * V scales count with magnitudes of 2^-100 to 2^100 (0 for a zero row).
+ */
+int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t kv_format, int32_t num_sms,
+                                decode_attn_plan* plan);
+size_t decode_attn_quant_workspace_size(const decode_attn_params* p, int32_t kv_format,
+                                        int device);
+int decode_attn_quant(const decode_attn_params* p, int32_t kv_format, const void* q,
+                      const void* k_pages, const void* v_pages, const float* k_scales,
+                      const float* v_scales, const int32_t* page_table, const int32_t* seq_lens,
+                      void* out, void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                      void* stream);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,9 @@ entry point without the built library raises.
 Entry points (same names as the C ABI):
   decode_attn, decode_attn_split, decode_attn_combine, decode_attn_host,
   decode_attn_workspace_size, decode_attn_make_plan, decode_attn_strerror;
-  decode_attn_chunk (attention of a ragged batch of new tokens)
+  decode_attn_chunk (attention of a ragged batch of new tokens);
+  decode_kv_append_chunk, decode_kv_read (a chunk's rows into a 16- or 8-bit
+  paged cache and back), decode_attn_quant (the decode step over an 8-bit one)
 """
 from __future__ import annotations
 
@@ -31,12 +33,15 @@ __all__ = [
     "decode_kv_append", "decode_attn_append", "DTYPE_FP16", "DTYPE_BF16",
     "SCHEDULE_AUTO", "SCHEDULE_GRID", "SCHEDULE_CLUSTER",
     "DecodeAttnChunkPlan", "decode_attn_chunk", "decode_attn_chunk_make_plan",
-    "decode_attn_chunk_workspace_size",
+    "decode_attn_chunk_workspace_size", "KV_16BIT", "KV_E4M3", "decode_kv_append_chunk",
+    "decode_kv_read", "decode_attn_quant", "decode_attn_quant_make_plan",
+    "decode_attn_quant_workspace_size",
 ]
 
 VARIANT_AUTO, VARIANT_SIMT, VARIANT_MMA = 0, 1, 2
 SCHEDULE_AUTO, SCHEDULE_GRID, SCHEDULE_CLUSTER = 0, 1, 2
 DTYPE_FP16, DTYPE_BF16 = 0, 1
+KV_16BIT, KV_E4M3 = 0, 1
 DEV_BAD_LEN, DEV_BAD_PAGE, DEV_OVER_HINT, DEV_TIMEOUT, DEV_WORKSPACE = 1, 2, 4, 8, 16
 DEV_CHECK = 32  # the checked build only: an index outside its buffer
 
@@ -129,6 +134,17 @@ def load_library():
             lib.decode_attn_chunk_workspace_size.restype = sz
             lib.decode_attn_chunk.argtypes = [PP, i32, P, P, P, P, P, P, P, P, sz, P, P]
             lib.decode_attn_chunk.restype = ctypes.c_int
+            lib.decode_kv_append_chunk.argtypes = [PP, i32, i32] + [P] * 11
+            lib.decode_kv_append_chunk.restype = ctypes.c_int
+            lib.decode_kv_read.argtypes = [PP, i32, i32] + [P] * 11
+            lib.decode_kv_read.restype = ctypes.c_int
+            lib.decode_attn_quant_make_plan.argtypes = [PP, i32, i32,
+                                                        ctypes.POINTER(DecodeAttnPlan)]
+            lib.decode_attn_quant_make_plan.restype = ctypes.c_int
+            lib.decode_attn_quant_workspace_size.argtypes = [PP, i32, ctypes.c_int]
+            lib.decode_attn_quant_workspace_size.restype = sz
+            lib.decode_attn_quant.argtypes = [PP, i32, P, P, P, P, P, P, P, P, P, sz, P, P]
+            lib.decode_attn_quant.restype = ctypes.c_int
             lib.decode_attn_strerror.argtypes = [ctypes.c_int]
             lib.decode_attn_strerror.restype = ctypes.c_char_p
             _lib = lib
@@ -581,4 +597,182 @@ def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, 
         _ptr(err_flag), _stream_handle(stream))
     if st:
         raise DecodeAttnError(st, "decode_attn_chunk")
+    return out
+
+
+def _kv_pools(k_pages, v_pages, k_scales, v_scales, device):
+    """The cell format of a pair of pools, after checking them (and the
+    scales an 8-bit pair needs)."""
+    import torch
+    if not isinstance(k_pages, torch.Tensor):
+        raise TypeError("k_pages must be a torch.Tensor")
+    quant = k_pages.dtype == torch.float8_e4m3fn
+    dt = k_pages.dtype if quant else _elem_dtype(k_pages)
+    _check(k_pages, dt, "k_pages", device)
+    _check(v_pages, dt, "v_pages", device)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [P, PS, Hkv, D], both of one shape")
+    P, PS, Hkv, _ = k_pages.shape
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if not quant:
+            if t is not None:
+                raise ValueError(f"{name} goes with float8_e4m3fn pools only")
+            continue
+        if t is None:
+            raise ValueError(f"float8_e4m3fn pools need {name}")
+        _check(t, torch.float32, name, device)
+        if tuple(t.shape) != (P, Hkv, PS):
+            raise ValueError(f"{name} must be [P, Hkv, PS] = [{P}, {Hkv}, {PS}]")
+    return KV_E4M3 if quant else KV_16BIT
+
+
+def _rows_params(k_pages, page_table, dtype_code: int) -> DecodeAttnParams:
+    P, PS, Hkv, D = k_pages.shape
+    return DecodeAttnParams(batch=page_table.shape[0], num_q_heads=Hkv, num_kv_heads=Hkv,
+                            head_dim=D, page_size=PS, max_pages_per_seq=page_table.shape[1],
+                            num_pages=P, scale=1.0, num_queries=1, dtype=dtype_code)
+
+
+@_on_device_of("k_pages", 4)
+def decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages, page_table,
+                           k_scales=None, v_scales=None, err_flag=None, stream=None):
+    """Writes a ragged batch's new rows k_new/v_new [total, Hkv, D] (fp16 or
+    bf16) into the pools: sequence b owns the rows row_offsets[b] to
+    row_offsets[b + 1] and they go to its last positions (seq_lens counts
+    them).  16-bit pools get the rows bit for bit; float8_e4m3fn pools get
+    codes, and k_scales/v_scales [P, Hkv, PS] float32 a power of two per row
+    and head."""
+    import torch
+    dev = k_pages.device
+    if dev.type != "cuda":
+        raise ValueError("decode_kv_append_chunk runs on CUDA tensors")
+    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    et = _elem_dtype(k_new) if fmt == KV_E4M3 else k_pages.dtype
+    _check(k_new, et, "k_new", dev)
+    _check(v_new, et, "v_new", dev)
+    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != tuple(k_pages.shape[2:]) or \
+            v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [total, Hkv, D]")
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch.Tensor")
+    _check_table(page_table, seq_lens, dev)
+    _check_offsets(row_offsets, page_table.shape[0], "row_offsets", dev)
+    _check_err_flag(err_flag, dev)
+    p = _rows_params(k_pages, page_table, _dtype_code(k_new))
+    st = load_library().decode_kv_append_chunk(
+        ctypes.byref(p), fmt, k_new.shape[0], _ptr(k_new), _ptr(v_new), _ptr(row_offsets),
+        _ptr(seq_lens), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+        _ptr(page_table), _ptr(err_flag), _stream_handle(stream))
+    if st:
+        raise DecodeAttnError(st, "decode_kv_append_chunk")
+
+
+@_on_device_of("k_pages", 0)
+def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, starts=None,
+                   k_scales=None, v_scales=None, dtype=None, k_out=None, v_out=None,
+                   err_flag=None, stream=None):
+    """Reads rows of the paged cache back as contiguous 16-bit rows: output
+    row row_offsets[b] + i is position starts[b] + i of sequence b (starts
+    None: from 0).  Returns (k, v), [total_rows, Hkv, D] of ``dtype`` (the
+    pools' own for 16-bit pools; by default float16 for float8_e4m3fn ones)
+    or k_out / v_out as given; rows that no sequence owns keep what they held
+    (new outputs are not initialised)."""
+    import torch
+    dev = k_pages.device
+    if dev.type != "cuda":
+        raise ValueError("decode_kv_read runs on CUDA tensors")
+    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    _check_table(page_table, None, dev)
+    B = page_table.shape[0]
+    _check_offsets(row_offsets, B, "row_offsets", dev)
+    if starts is not None:
+        _check(starts, torch.int32, "starts", dev)
+        if tuple(starts.shape) != (B,):
+            raise ValueError(f"starts must be [B] = [{B}]")
+    _check_err_flag(err_flag, dev)
+    if dtype is None:
+        given = k_out if k_out is not None else v_out
+        dtype = k_pages.dtype if fmt == KV_16BIT else \
+            given.dtype if given is not None else torch.float16
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"expected float16 or bfloat16 outputs, got {dtype}")
+    if fmt == KV_16BIT and dtype != k_pages.dtype:
+        raise TypeError(f"16-bit pools are read back as they are ({k_pages.dtype})")
+    shape = (int(total_rows), *k_pages.shape[2:])
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        _check(t, dtype, name, dev)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
+        outs.append(t)
+    p = _rows_params(k_pages, page_table, _dtype_code(outs[0]))
+    st = load_library().decode_kv_read(
+        ctypes.byref(p), fmt, shape[0], _ptr(k_pages), _ptr(v_pages), _ptr(k_scales),
+        _ptr(v_scales), _ptr(page_table), _ptr(row_offsets), _ptr(starts), _ptr(outs[0]),
+        _ptr(outs[1]), _ptr(err_flag), _stream_handle(stream))
+    if st:
+        raise DecodeAttnError(st, "decode_kv_read")
+    return outs[0], outs[1]
+
+
+def decode_attn_quant_make_plan(params: DecodeAttnParams, num_sms: int,
+                                kv_format: int = KV_E4M3) -> DecodeAttnPlan:
+    plan = DecodeAttnPlan()
+    st = load_library().decode_attn_quant_make_plan(ctypes.byref(params), int(kv_format),
+                                                    int(num_sms), ctypes.byref(plan))
+    if st:
+        raise DecodeAttnError(st, "decode_attn_quant_make_plan")
+    return plan
+
+
+def decode_attn_quant_workspace_size(params: DecodeAttnParams, device: int,
+                                     kv_format: int = KV_E4M3) -> int:
+    return int(load_library().decode_attn_quant_workspace_size(
+        ctypes.byref(params), int(kv_format), int(device)))
+
+
+@_on_device_of("q", 0)
+def decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens,
+                      scale: float, window: int = 0, out=None,
+                      max_seq_len: Optional[int] = None, workspace=None, err_flag=None,
+                      split_min: int = 0, force_chunk: int = 0, stream=None,
+                      schedule: int = SCHEDULE_AUTO):
+    """decode_attn over an 8-bit cache: k_pages/v_pages [P, PS, Hkv, D]
+    float8_e4m3fn with k_scales/v_scales [P, Hkv, PS] float32 (value = code *
+    scale).  q [B, Hq, D] (or [B, T, Hq, D]) fp16 or bf16; returns ``out``
+    like q."""
+    import torch
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("decode_attn_quant runs on CUDA tensors")
+    et = _elem_dtype(q)
+    _check(q, et, "q", dev)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, T, Hq, D]")
+    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    if fmt != KV_E4M3:
+        raise TypeError(f"decode_attn_quant takes float8_e4m3fn pools, got {k_pages.dtype}")
+    _check_table(page_table, seq_lens, dev)
+    if page_table.shape[0] != q.shape[0]:
+        raise ValueError("page_table must have a row for each sequence of q")
+    _check_err_flag(err_flag, dev)
+    p = make_params(q, k_pages, page_table, scale, window, max_seq_len, VARIANT_AUTO, split_min,
+                    force_chunk, schedule)
+    if out is None:
+        out = torch.empty_like(q)
+    _check(out, et, "out", dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = _scratch(dev, decode_attn_quant_workspace_size(
+            p, dev.index if dev.index is not None else torch.cuda.current_device()), True, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load_library().decode_attn_quant(
+        ctypes.byref(p), fmt, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales),
+        _ptr(v_scales), _ptr(page_table), _ptr(seq_lens), _ptr(out), _ptr(workspace), ws_bytes,
+        _ptr(err_flag), _stream_handle(stream))
+    if st:
+        raise DecodeAttnError(st, "decode_attn_quant")
     return out

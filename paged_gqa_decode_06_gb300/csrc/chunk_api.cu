@@ -41,6 +41,7 @@ int run_chunk(const decode_attn_params* p, const decode_attn_chunk_plan& plan, i
   a.page_table = page_table;
   a.offsets = query_offsets;
   a.seq_lens = seq_lens;
+  a.v_pages = v_pages;
   a.out = out;
   a.err = err_flag;
   a.B = p->batch;

@@ -26,6 +26,13 @@
 // K as K-major with D * 16 bytes between groups of 8 tokens, V as MN-major
 // with 1024 bytes between chunks of 64 dims.
 //
+// Keys that only some rows of the CTA attend (the diagonal, a window's start,
+// a page's unused positions) lie in the edge tiles.  There the mask is
+// applied score by score, and two more warps look V over before its product:
+// what no row attends becomes zero, and a NaN or Inf is set to zero and added
+// in the epilogue to the rows that attend it, since a product with a weight of
+// zero would carry it to the others.
+//
 // P is rounded once to the element type for the second product (the weights
 // of a row are at most 2^8 and the largest is at least 1, so each keeps that
 // type's relative precision); sums, maxima and accumulators are fp32.
@@ -44,6 +51,7 @@ struct ChunkArgs {
   const int32_t* page_table;  // [B][max_pages]
   const int32_t* offsets;     // [B + 1] rows of each sequence
   const int32_t* seq_lens;    // [B]
+  const void* v_pages;
   void* out;                  // [total][Hq][D]
   float* ws_acc;              // [total * Hq][max_shards][D]   (split plans)
   float2* ws_ml;              // [total * Hq][max_shards]; l = -1 marks a bad row
@@ -70,6 +78,9 @@ struct ChunkCfg {
   static constexpr int kRing = D == 64 ? 8 : 5;
   static constexpr int kSmemBytes = kStreams * kQBytes + kRing * kTileBytes + 1024;
   static constexpr uint32_t kTmemCols = 512;
+  // edge tiles of one CTA: the diagonal and a window's start each cross at
+  // most 3 tiles (256 tokens, 128 at D = 256)
+  static constexpr int kMaxEdges = 8;
 };
 
 // One CTA's share of the work, found from its slot.
@@ -119,6 +130,13 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, in
   return it;
 }
 
+// A bit per 16-bit value of w that is not finite (all of its bits set).
+template <class E>
+__device__ __forceinline__ uint32_t wild2(uint32_t w) {
+  constexpr uint32_t kExp = std::is_same<E, __nv_bfloat16>::value ? 0x7f807f80u : 0x7c007c00u;
+  return __vcmpeq2(w & kExp, kExp);
+}
+
 template <int D>
 __device__ __forceinline__ uint64_t k_desc(uint32_t tile) {
   return tc_desc(tile, 16, D * 16);
@@ -142,10 +160,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full, full_bar[NR], empty_bar[NR];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[NS];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[NS], v_edge, v_clean;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int32_t abort_s;
   __shared__ int32_t bad_lo_s, bad_hi_s;  // positions in pages outside the pool
+  // keys of the edge tiles whose V row is not finite
+  __shared__ uint32_t wild_s[C::kMaxEdges][KT / 32];
+  __shared__ int32_t edge_key_s[C::kMaxEdges], wild_any_s;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -166,11 +187,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       mbar_init(smem_u32(&p_full[i]), 4);
     }
     for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&o_full[i]), 1);
+    mbar_init(smem_u32(&v_edge), 1);
+    mbar_init(smem_u32(&v_clean), 2);
     fence_mbar_init();
     abort_s = 0;
     bad_lo_s = INT32_MAX;
     bad_hi_s = -1;
+    wild_any_s = 0;
   }
+  for (int i = threadIdx.x; i < C::kMaxEdges * KT / 32; i += C::kThreads)
+    wild_s[i / (KT / 32)][i % (KT / 32)] = 0u;
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
@@ -203,6 +229,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const int key0 = it.base + tile0 * KT;  // first key of this CTA's first tile
   const int ns = (it.t1 - it.t0) > a.tile_tok ? NS : 1;  // streams with tokens
   const int units = ntiles * ns;
+  // whether some row of the CTA does not attend all of tile j
+  const int plast = it.p0 + (it.t1 - it.t0) - 1;
+  auto edge = [&](int j) {
+    const int k0 = key0 + j * KT;
+    return k0 + KT - 1 > it.p0 || (a.window > 0 && k0 <= plast - a.window);
+  };
 
   // two streams: 384 threads launched with 168 registers each; the row
   // threads (a row of 128 scores apiece) take 224, the last warpgroup 56
@@ -293,7 +325,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           tc_fence_after();
           const uint64_t qd = tc_desc(smem_u32(smem + s * C::kQBytes), 16, 1024);
           const uint64_t kd = k_desc<D>(smem_u32(ring + (r % NR) * C::kTileBytes));
-  #pragma unroll
+#pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const int c = ks >> 2, in = (ks & 3) * 2;  // 32 bytes inside a 64-dim chunk
             tc_mma_ss(tmem + (u & 1) * KT, qd + c * (128 * 128 / 16) + in, kd + c * (1024 / 16) + in,
@@ -307,32 +339,21 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       wait(&q_full, 0);
       issue_s(0);
       if (units > 1) issue_s(1);
+      int edges = 0;
       for (int u = 0; u < units && ok; ++u) {
         const int j = u / ns, s = u % ns, r = 2 * j + 1;
         uint8_t* vt = ring + (r % NR) * C::kTileBytes;
         if (s == 0) {
           wait(&full_bar[r % NR], (r / NR) & 1);
-          // V rows of the tile outside the attended range (a page's other
-          // positions) become zeros: a zero weight must not meet a NaN
-          const int k0 = key0 + j * KT;
-          if (ok && (k0 < it.lo || k0 + KT > it.hi)) {
-            for (int e = lane; e < KT * (D / 8); e += 32) {
-              const int t = e / (D / 8), c = e % (D / 8);
-              if (k0 + t < it.lo || k0 + t >= it.hi)
-                *reinterpret_cast<uint4*>(vt + (t >> 3) * (D * 16) + (c >> 3) * 1024 +
-                                          (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
+          if (ok && edge(j) && lane == 0) mbar_arrive(smem_u32(&v_edge));
         }
         wait(&p_full[u & 1], (u >> 1) & 1);
+        if (s == 0 && edge(j)) wait(&v_clean, edges++ & 1);
         if (!ok) break;
         if (lane == 0) {
           tc_fence_after();
           const uint64_t vd = v_desc<D>(smem_u32(vt));
-  #pragma unroll
+#pragma unroll
           for (int ks = 0; ks < KT / 16; ++ks)  // O += P . V
             tc_mma_ts(tmem_o + s * D, tmem + (u & 1) * KT + ks * 8, vd + ks * (D * 32 / 16), kIdescO,
                       j > 0 || ks > 0);
@@ -345,8 +366,38 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       named_barrier_sync(1, kOthers);  // every row has been read out
       tc_fence_after();
       tmem_free(tmem, C::kTmemCols);
+      return;
     }
-    return;  // (two more warps only fill the warpgroup)
+    // the two warps that look over V's edge tiles
+    int edges = 0;
+    for (int j = 0; j < ntiles; ++j) {
+      if (!edge(j)) continue;
+      if (!mbar_wait(smem_u32(&v_edge), edges & 1)) abort_s = 1;
+      if (!__all_sync(0xffffffffu, !abort_s)) break;
+      const int k0 = key0 + j * KT;
+      uint8_t* vt = ring + ((2 * j + 1) % NR) * C::kTileBytes;
+      if (warp == kMma + 1 && lane == 0 && edges < C::kMaxEdges) edge_key_s[edges] = k0;
+#pragma unroll 4
+      for (int e = (warp - kMma - 1) * 32 + lane; e < C::kTileBytes / 16; e += 64) {
+        const int t = e / D * 8 + (e % 64) / 8;  // groups of 8 tokens, 1 KB per 64 dims
+        uint4* at = reinterpret_cast<uint4*>(vt) + e;
+        if (k0 + t < it.lo || k0 + t >= it.hi) {
+          *at = make_uint4(0u, 0u, 0u, 0u);
+          continue;
+        }
+        const uint4 v = *at;
+        const uint4 m = make_uint4(wild2<E>(v.x), wild2<E>(v.y), wild2<E>(v.z), wild2<E>(v.w));
+        if ((m.x | m.y | m.z | m.w) == 0u) continue;
+        *at = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
+        if (edges < C::kMaxEdges) atomicOr(&wild_s[edges][t / 32], 1u << (t & 31));
+        wild_any_s = 1;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&v_clean));
+      ++edges;
+    }
+    return;
   }
 
   // ---------------------------------------------------------- softmax rows
@@ -472,6 +523,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const bool dead = !ok || (pos >= bad_lo_s && (a.window <= 0 || pos - a.window + 1 < bad_hi_s));
     const size_t orow = (size_t)(it.row0 + s * a.tile_tok + tok) * a.Hq + (size_t)h * a.G + g;
     const bool in = live && PGD_IN(orow, (size_t)a.total * a.Hq, a.err);
+    // V rows with a NaN or Inf reach the rows that attend them
+    auto patch = [&](int c, float (&o)[32]) {
+      for (int e = 0; e < C::kMaxEdges; ++e)
+        for (int t = 0; t < KT; ++t) {
+          const int key = edge_key_s[e] + t;
+          if (!(wild_s[e][t / 32] >> (t & 31) & 1u) || key > pos ||
+              (a.window > 0 && key <= pos - a.window))
+            continue;
+          const size_t pi = (size_t)it.b * a.max_pages + (key >> a.page_shift);
+          const int phys = PGD_IN(pi, (size_t)a.B * a.max_pages, a.err) ? a.page_table[pi] : -1;
+          if (phys < 0 || phys >= a.num_pages) continue;
+          const uint32_t* v = static_cast<const uint32_t*>(a.v_pages) +
+                              ((((size_t)phys << a.page_shift) + (key & (a.page_size - 1))) *
+                                   a.Hkv + h) * (D / 2) + c / 2;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t w = __ldg(v + i);
+            const float2 f = ElemOps<E>::unpack2(w & wild2<E>(w));
+            o[2 * i] += f.x;
+            o[2 * i + 1] += f.y;
+          }
+        }
+    };
     if (it.shards == 1) {
       const float inv = dead || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D);
@@ -481,6 +555,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         if (ok) tmem_ld32(o, tmem_o + s * D + lanes + c);
         tmem_wait_ld();
         if (!in) continue;
+        if (wild_any_s) patch(c, o);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
 #pragma unroll
@@ -500,6 +575,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         if (ok) tmem_ld32(o, tmem_o + s * D + lanes + c);
         tmem_wait_ld();
         if (!in || dead) continue;
+        if (wild_any_s) patch(c, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           dst[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);

@@ -1,0 +1,553 @@
+// Decode attention over an 8-bit cache (e4m3 codes, one fp32 scale per
+// (position, KV head) row of K and of V): out = sum_t p_t vs_t vc_t with
+// scores scale * ks_t * (q . kc_t).
+//
+// The shape of the 16-bit split kernel (split_mma.cuh): one CTA per (shard,
+// KV head, sequence), a producer warp filling a shared-memory ring by TMA,
+// four consumer warps of 16 positions each, mma.sync with the tokens on M and
+// the group's query rows on N, and the same merges (workspace, or a cluster's
+// distributed shared memory).  What differs is what a stage holds and how the
+// fragments come out of it:
+//  * A stage is 64 positions of codes (half the bytes), so twice the stages
+//    are in flight; the scales of its positions follow by cp.async, 16 bytes
+//    (4 positions of one head; they lie [P][Hkv][PS]) per lane.
+//  * Codes become fp16 in registers, exactly: ldmatrix moves pairs of codes,
+//    a K register of four dims gives two A registers (the order of the
+//    contraction is free, so q is loaded in the same order), and a transposed
+//    V register of (2 tokens x 2 dims) gives, after two conversions and two
+//    byte permutations, the registers of two output dims.
+//  * The products are fp16 for either element type of q: a bf16 row of q is
+//    scaled by a power of two to magnitudes below 2, which fp16 holds to
+//    2^-25 of the row's largest, and the scores take the factor back.
+//  * The scales enter in fp32, ks with the scores.  vs goes into the weight
+//    w_t = p_t vs_t: the running maximum is taken over log2(p_t vs_t), so
+//    that w_t <= 1 whatever the magnitude of V, while the sum keeps p_t.  w is
+//    split into an fp16 head and remainder (two products), about 22 bits.
+#pragma once
+
+#include <type_traits>
+
+#include "e4m3.cuh"
+#include "split_mma.cuh"
+
+namespace pgd {
+
+struct QuantArgs {
+  SplitArgs s;            // as for the 16-bit split kernel
+  const float* k_scales;  // [P][Hkv][PS]
+  const float* v_scales;
+};
+
+template <int D>
+struct QuantCfg {
+  static constexpr int kWarps = 4;
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kWidth = D < 128 ? D : 128;   // bytes of a swizzled row
+  static constexpr int kTileBytes = kTile * D;       // K or V codes of a stage
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = 96 * 1024 / kStageBytes;  // 12, 6, 3
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kRingBytes + 1024;
+};
+
+// Byte offset of (token t, 16-byte chunk c) in a tile of codes made of pieces
+// of 2^ps rows, each [D / kWidth][2^ps rows][kWidth] with the 128-byte (or at
+// D = 64 the 64-byte) swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t code_offset(int t, int c, int ps) {
+  constexpr int W = QuantCfg<D>::kWidth, kChunks = W / 16;
+  const int rows = 1 << ps, r = t & (rows - 1);
+  const int key = W == 128 ? (r & 7) : ((r >> 1) & 3);
+  return (uint32_t)((t >> ps) * (rows * D) + (c / kChunks) * (rows * W) + r * W +
+                    (((c % kChunks) ^ key) << 4));
+}
+
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
+  return __byte_perm(a, b, sel);
+}
+
+// log2 of a V scale for the running maximum; clamped, so that a zero row
+// (scale 0) neither wins it nor makes a sum overflow.
+__device__ __forceinline__ float scale_log2_of(float v) {
+  const float a = fminf(fmaxf(fabsf(v), 7.8886e-31f), 1.2677e30f);  // 2^-100, 2^100
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(a));
+  return y;
+}
+
+// One consumer warp's 16 positions of a staged tile (K codes at kt, V codes
+// behind them, ks / vs the stage's scales): mma_block's counterpart.
+template <int D, int NT8>
+__device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, const float* vs_s,
+                                            int warp, int lane, int tok0, int lo, int hi,
+                                            const int (&col_lo)[NT8][2],
+                                            const int (&col_hi)[NT8][2],
+                                            const uint32_t (&qf)[NT8][D / 16][2],
+                                            const float (&col_scale)[NT8][2],
+                                            float (&acc)[D / 16][NT8][4], float (&m_run)[NT8][2],
+                                            float (&l_part)[NT8][2], int ps) {
+  using H = ElemOps<__half>;
+  const int gid = lane >> 2;
+  const int mat = lane >> 3, mrow = lane & 7;
+  const int tok = 16 * warp + mrow + ((mat & 1) ? 8 : 0);  // matrix bit 0: tokens 8..15
+  const int half = mat >> 1;                               // matrix bit 1: dims 16..31
+  const uint32_t kbase = smem_u32(kt);
+  const uint32_t vbase = kbase + QuantCfg<D>::kTileBytes;
+  if (tok0 < lo || tok0 + 16 > hi) {
+    // V codes outside the range become zeros: a zero weight meets no NaN
+    uint8_t* vt = kt + QuantCfg<D>::kTileBytes;
+    for (int e = lane; e < 16 * (D / 16); e += 32) {
+      const int t = e / (D / 16), c = e % (D / 16);
+      if (tok0 + t < lo || tok0 + t >= hi)
+        *reinterpret_cast<uint4*>(vt + code_offset<D>(16 * warp + t, c, ps)) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  float sc[NT8][4];
+#pragma unroll
+  for (int j = 0; j < NT8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+  for (int kb = 0; kb < D / 32; ++kb) {
+    uint32_t r[4];  // (tokens 0-7, 8-15) x (dims 0-15, 16-31): four dims per register
+    ldmatrix_x4(r, kbase + code_offset<D>(tok, 2 * kb + half, ps));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t af[4] = {e4m3_to_half2(r[2 * i] & 0xffffu),
+                              e4m3_to_half2(r[2 * i + 1] & 0xffffu),
+                              e4m3_to_half2(r[2 * i] >> 16), e4m3_to_half2(r[2 * i + 1] >> 16)};
+#pragma unroll
+      for (int j = 0; j < NT8; ++j) H::mma(sc[j], af, qf[j][2 * kb + i][0], qf[j][2 * kb + i][1]);
+    }
+  }
+  const int tok_a = tok0 + gid, tok_b = tok0 + gid + 8;
+  const float ks_a = ks_s[16 * warp + gid], ks_b = ks_s[16 * warp + gid + 8];
+  const float vs_a = vs_s[16 * warp + gid], vs_b = vs_s[16 * warp + gid + 8];
+  const float lv_a = scale_log2_of(vs_a), lv_b = scale_log2_of(vs_b);
+  uint32_t pb_hi[NT8][2], pb_lo[NT8][2];
+  bool rescale = false;
+  float alpha[NT8][2];
+#pragma unroll
+  for (int j = 0; j < NT8; ++j) {
+    float w[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool in_a = tok_a >= col_lo[j][e] && tok_a < col_hi[j][e];
+      const bool in_b = tok_b >= col_lo[j][e] && tok_b < col_hi[j][e];
+      const float sa = in_a ? sc[j][e] * (col_scale[j][e] * ks_a) : -INFINITY;
+      const float sb = in_b ? sc[j][e + 2] * (col_scale[j][e] * ks_b) : -INFINITY;
+      float mx = fmaxf(in_a ? sa + lv_a : -INFINITY, in_b ? sb + lv_b : -INFINITY);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float m_new = fmaxf(m_run[j][e], mx);
+      alpha[j][e] = (m_new == -INFINITY) ? 1.f : fast_exp2(m_run[j][e] - m_new);
+      rescale |= alpha[j][e] != 1.f;
+      const float pa = in_a ? fast_exp2(sa - m_new) : 0.f;
+      const float pb = in_b ? fast_exp2(sb - m_new) : 0.f;
+      l_part[j][e] = l_part[j][e] * alpha[j][e] + pa + pb;
+      m_run[j][e] = m_new;
+      w[e] = in_a ? pa * vs_a : 0.f;
+      w[e + 2] = in_b ? pb * vs_b : 0.f;
+    }
+    const uint32_t h0 = H::pack2(w[0], w[1]), h1 = H::pack2(w[2], w[3]);
+    const float2 f0 = H::unpack2(h0), f1 = H::unpack2(h1);
+    pb_hi[j][0] = movmatrix_trans(h0);
+    pb_hi[j][1] = movmatrix_trans(h1);
+    pb_lo[j][0] = movmatrix_trans(H::pack2(w[0] - f0.x, w[1] - f0.y));
+    pb_lo[j][1] = movmatrix_trans(H::pack2(w[2] - f1.x, w[3] - f1.y));
+  }
+  if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+    for (int mi = 0; mi < D / 16; ++mi)
+#pragma unroll
+      for (int j = 0; j < NT8; ++j) {
+        acc[mi][j][0] *= alpha[j][0];
+        acc[mi][j][1] *= alpha[j][1];
+        acc[mi][j][2] *= alpha[j][0];
+        acc[mi][j][3] *= alpha[j][1];
+      }
+  }
+  // out^T += V^T . W^T: row gid of a tile of 16 dims is dim 2 gid, row gid + 8
+  // dim 2 gid + 1
+#pragma unroll
+  for (int kb = 0; kb < D / 32; ++kb) {
+    uint32_t r[4];  // as for K, transposed: (2 tokens x 2 dims) per register
+    ldmatrix_x4_trans(r, vbase + code_offset<D>(tok, 2 * kb + half, ps));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a0 = e4m3_to_half2(r[2 * i] & 0xffffu), a1 = e4m3_to_half2(r[2 * i] >> 16);
+      const uint32_t b0 = e4m3_to_half2(r[2 * i + 1] & 0xffffu),
+                     b1 = e4m3_to_half2(r[2 * i + 1] >> 16);
+      const uint32_t af[4] = {byte_perm(a0, a1, 0x5410), byte_perm(a0, a1, 0x7632),
+                              byte_perm(b0, b1, 0x5410), byte_perm(b0, b1, 0x7632)};
+#pragma unroll
+      for (int j = 0; j < NT8; ++j) {
+        H::mma(acc[2 * kb + i][j], af, pb_hi[j][0], pb_hi[j][1]);
+        H::mma(acc[2 * kb + i][j], af, pb_lo[j][0], pb_lo[j][1]);
+      }
+    }
+  }
+}
+
+// A row of q as fp16 fragments, 4 consecutive dims per lane and 16-dim step;
+// returns the power of two taken out of a bf16 row.
+template <int D, class E>
+__device__ __forceinline__ float load_q_row(const uint16_t* row, bool live, int tig,
+                                            uint32_t (&qf)[D / 16][2]) {
+  uint2 raw[D / 16];
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    raw[ks] = live ? *reinterpret_cast<const uint2*>(row + ks * 16 + 4 * tig) : make_uint2(0u, 0u);
+  if constexpr (std::is_same<E, __half>::value) {
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qf[ks][0] = raw[ks].x;
+      qf[ks][1] = raw[ks].y;
+    }
+    return 1.f;
+  } else {
+    float amax = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const float2 a = ElemOps<E>::unpack2(raw[ks].x), b = ElemOps<E>::unpack2(raw[ks].y);
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^E of the row's largest value (a tiny row stays, an Inf stays Inf)
+    const uint32_t e = min(max((__float_as_uint(amax) >> 23) & 255u, 27u), 253u);
+    const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const float2 a = ElemOps<E>::unpack2(raw[ks].x), b = ElemOps<E>::unpack2(raw[ks].y);
+      qf[ks][0] = ElemOps<__half>::pack2(a.x * inv, a.y * inv);
+      qf[ks][1] = ElemOps<__half>::pack2(b.x * inv, b.y * inv);
+    }
+    return __uint_as_float(e << 23);
+  }
+}
+
+// CL: a cluster plan, as in split_mma_body.
+template <int D, int NT8, class E, bool CL>
+__global__ void __launch_bounds__(QuantCfg<D>::kThreads)
+    quant_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const QuantArgs qa) {
+  using C = QuantCfg<D>;
+  constexpr int KS = D / 16, kWarps = C::kWarps, GP = 8 * NT8;
+  const SplitArgs& a = qa.s;
+
+  __shared__ __align__(8) uint64_t full_bar[C::kStages];
+  __shared__ __align__(8) uint64_t empty_bar[C::kStages];
+  __shared__ __align__(8) uint64_t recv_bar;
+  __shared__ __align__(16) float scale_s[C::kStages][2][kTile];
+  __shared__ int32_t coord_s[kMaxPieces];
+  __shared__ float2 ml_s[kWarps][GP];
+  __shared__ float cw_s[kWarps][GP];
+  __shared__ float2 row_s[GP];
+  __shared__ int32_t bad_s;
+  __shared__ volatile int32_t abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = ring_base();
+
+  if (threadIdx.x == kWarps * 32) {
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+    for (int st = 0; st < C::kStages; ++st) {
+      // the boxes' arrival, and one of each producer lane for its scales
+      mbar_init(smem_u32(&full_bar[st]), 1 + 32);
+      mbar_init(smem_u32(&empty_bar[st]), kWarps);
+    }
+    if constexpr (CL) mbar_init(smem_u32(&recv_bar), cluster_size());
+    fence_mbar_init();
+    abort_s = 0;
+    bad_s = 0;
+  }
+  __syncthreads();
+  if constexpr (CL) cluster_arrive_relaxed();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int h = a.head_fastest ? blockIdx.x : blockIdx.y;
+  const int s = a.head_fastest ? blockIdx.y : blockIdx.x;
+  const int b = blockIdx.z;
+  const int capacity = a.max_pages * a.page_size;
+  const int box_t = a.box_tokens;
+  // page ids of the first 32 pieces, read together with the length under the
+  // guess that the sequence is as long as the plan's bound
+  int spec_lo = -1, spec_phys = -1;
+  if (warp == kWarps) {
+    const SeqRange g =
+        seq_range(a.len_hint, a.window, capacity, a.chunk, a.max_shards, a.T, a.balanced);
+    if (g.status == 0 && s < g.nshards) {
+      spec_lo = g.base + s * g.chunk;
+      const int ptok = spec_lo + lane * box_t;
+      const size_t pi = (size_t)b * a.max_pages + (ptok >> a.page_shift);
+      if (ptok < capacity && PGD_IN(pi, (size_t)a.batch * a.max_pages, a.err))
+        spec_phys = ld_global_s32(a.page_table + pi);
+    }
+  }
+  const SeqRange r = seq_range(ld_global_s32(a.seq_lens + b), a.window, capacity, a.chunk,
+                               a.max_shards, a.T, a.balanced);
+  const int R = a.T * a.G;
+  const int gid = lane >> 2, tig = lane & 3;
+  uint8_t* recv = ring + C::kRingBytes;
+
+  if (r.status != 0 || s >= r.nshards) {
+    if (s == 0 && r.status != 0 && threadIdx.x == 0) raise_error(a.err, r.status);
+    if constexpr (CL) {
+      if (warp < kWarps) {  // an empty partial still takes part in the exchange
+        const ClusterXchg x(recv, R, D);
+        cluster_wait();
+        for (int e = threadIdx.x; e < R * (D / 4); e += kWarps * 32)
+          x.push(e, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int g = threadIdx.x; g < R; g += kWarps * 32)
+          x.push_ml(g, make_float2(-INFINITY, 0.f));
+        cluster_finish<D, E>(a, x, b, h, smem_u32(&recv_bar), recv, kWarps * 32);
+      }
+    } else if (s == 0) {
+      zero_group_rows<D, GP>(a, b, h);
+    }
+    return;
+  }
+
+  const int shard_lo = r.base + s * r.chunk;
+  const int lo = max(r.start, shard_lo);
+  const int hi = min(r.end, shard_lo + r.chunk);
+  const int n_tiles = (hi - shard_lo + kTile - 1) / kTile;
+  const int pieces = kTile / box_t, n_pieces = n_tiles * pieces;
+
+  if (warp == kWarps) {
+    const int pool_rows = a.num_pages * a.page_size;  // past the pool: zeros
+    int any_bad = 0;
+#pragma unroll 4
+    for (int i = lane; i < n_pieces; i += 32) {
+      const int ptok = shard_lo + i * box_t;
+      int coord = pool_rows;
+      if (ptok < hi && ptok + box_t > lo) {
+        int phys;
+        if (i == lane && shard_lo == spec_lo) {
+          phys = spec_phys;
+        } else {
+          const size_t pi = (size_t)b * a.max_pages + (ptok >> a.page_shift);
+          phys = PGD_IN(pi, (size_t)a.batch * a.max_pages, a.err) ? a.page_table[pi] : -1;
+        }
+        if (phys < 0 || phys >= a.num_pages)
+          any_bad = 1;
+        else
+          coord = phys * a.page_size + (ptok & (a.page_size - 1));
+      }
+      coord_s[i] = coord;
+    }
+    if (__any_sync(0xffffffffu, any_bad)) {
+      // no copy is issued; the consumers' first wait completes on plain
+      // arrivals and they find the flag
+      if (lane == 0) {
+        bad_s = 1;
+        raise_error(a.err, DECODE_ATTN_DEV_BAD_PAGE);
+      }
+      __syncwarp();
+      mbar_arrive(smem_u32(&full_bar[0]));
+      if (lane == 0) mbar_arrive(smem_u32(&full_bar[0]));
+      return;
+    }
+    __syncwarp();
+    const uint64_t policy = l2_evict_first_policy();
+    const float* scales = lane < 16 ? qa.k_scales : qa.v_scales;
+    int issued = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int st = i % C::kStages;
+      if (i >= C::kStages) {
+        int go = 1;
+        if (lane == 0) {
+          if (!mbar_wait(smem_u32(&empty_bar[st]), ((i / C::kStages) & 1) ^ 1)) {
+            abort_s = 1;
+            raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+          }
+          go = abort_s ? 0 : 1;
+        }
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      }
+      const uint32_t fb = smem_u32(&full_bar[st]);
+      if (lane == 0) mbar_arrive_expect_tx(fb, C::kStageBytes + (i == 0 ? a.stall_tx : 0));
+      __syncwarp();
+      if (lane < 2 * pieces) {  // at most 16 boxes: pieces of 8 positions or more
+        const int coord = coord_s[i * pieces + (lane >> 1)];
+        const bool in = PGD_IN(coord == pool_rows ? 0 : (int64_t)coord + box_t - 1, pool_rows, a.err);
+        tma_load_4d_hint(smem_u32(ring + st * C::kStageBytes) + (lane & 1) * C::kTileBytes +
+                             (lane >> 1) * box_t * D,
+                         (lane & 1) ? &tmap_v : &tmap_k, 0, in ? coord : pool_rows, h, 0, fb,
+                         policy);
+      }
+      {
+        // this lane's 4 positions' scales (lanes 0-15 K, 16-31 V); zeros
+        // where no position is attended
+        const int t = 4 * (lane & 15);
+        const int coord = coord_s[i * pieces + t / box_t];
+        const bool in = coord < pool_rows;
+        const int row = (in ? coord : 0) + (in ? t % box_t : 0);
+        const size_t at = ((size_t)(row >> a.page_shift) * a.Hkv + h) * a.page_size +
+                          (row & (a.page_size - 1));
+        const bool ok = PGD_IN(at + 3, (size_t)pool_rows * a.Hkv, a.err);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(&scale_s[st][lane >> 4][t])),
+                     "l"(scales + (ok ? at : 0)), "r"(in && ok ? 16 : 0)
+                     : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+      }
+      issued = i + 1;
+    }
+    // this CTA's copies in flight have landed before the warp exits
+    for (int i = max(0, issued - C::kStages); i < issued; ++i)
+      mbar_wait(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1);
+    return;
+  }
+
+  // ------------------------------------------------------------ consumers
+  uint32_t qf[NT8][KS][2];
+  float acc[KS][NT8][4];
+  int col_lo[NT8][2], col_hi[NT8][2];
+  float m_run[NT8][2], l_part[NT8][2], col_scale[NT8][2];
+#pragma unroll
+  for (int j = 0; j < NT8; ++j) {
+    const int rr = 8 * j + gid;
+    size_t qr = group_row(b, h, rr < R ? rr : 0, a.T, a.G, a.Hq);
+    if (!PGD_IN(qr, (size_t)a.batch * a.T * a.Hq, a.err)) qr = 0;
+    const float f =
+        load_q_row<D, E>(static_cast<const uint16_t*>(a.q) + qr * D, rr < R, tig, qf[j]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // this lane's score columns are rows 8j + 2 tig + e
+      col_scale[j][e] = a.scale_log2 * __shfl_sync(0xffffffffu, f, (2 * tig + e) * 4);
+      const int cr = 8 * j + 2 * tig + e;
+      const int t = cr < R ? cr / a.G : a.T - 1;
+      col_hi[j][e] = r.end - a.T + t + 1;
+      col_lo[j][e] = a.window > 0 ? max(0, col_hi[j][e] - a.window) : 0;
+      m_run[j][e] = -INFINITY;
+      l_part[j][e] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int mi = 0; mi < KS; ++mi)
+#pragma unroll
+    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[mi][j][e] = 0.f;
+  const int piece_shift = __ffs(box_t) - 1;
+  for (int i = 0; i < n_tiles; ++i) {
+    const int st = i % C::kStages;
+    if (!mbar_wait(smem_u32(&full_bar[st]), (i / C::kStages) & 1)) {
+      abort_s = 1;
+      raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+      break;
+    }
+    if (bad_s || abort_s) break;
+    const int tok0 = shard_lo + i * kTile + 16 * warp;
+    if (tok0 + 16 > lo && tok0 < hi)
+      quant_block<D, NT8>(ring + st * C::kStageBytes, scale_s[st][0], scale_s[st][1], warp, lane,
+                          tok0, lo, hi, col_lo, col_hi, qf, col_scale, acc, m_run, l_part,
+                          piece_shift);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));
+  }
+
+  // ---- fold the consumer warps in fixed order (deterministic) -----------
+#pragma unroll
+  for (int j = 0; j < NT8; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = l_part[j][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      l_part[j][e] = l;
+    }
+  named_barrier_sync(1, kWarps * 32);  // every consumer is done with the ring
+  constexpr int kRowStride = D + 4;
+  static_assert(kWarps * GP * kRowStride * 4 <= C::kRingBytes, "warp states fit in the ring");
+  float* acc_s = reinterpret_cast<float*>(ring);
+  if (gid == 0) {
+#pragma unroll
+    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        ml_s[warp][8 * j + 2 * tig + e] = make_float2(m_run[j][e], l_part[j][e]);
+  }
+#pragma unroll
+  for (int mi = 0; mi < KS; ++mi)
+#pragma unroll
+    for (int j = 0; j < NT8; ++j) {
+      const int hd = 8 * j + 2 * tig, d = 16 * mi + 2 * gid;
+      float* base = acc_s + (warp * GP) * kRowStride;
+      *reinterpret_cast<float2*>(base + hd * kRowStride + d) =
+          make_float2(acc[mi][j][0], acc[mi][j][2]);
+      *reinterpret_cast<float2*>(base + (hd + 1) * kRowStride + d) =
+          make_float2(acc[mi][j][1], acc[mi][j][3]);
+    }
+  named_barrier_sync(1, kWarps * 32);
+  if (threadIdx.x < R) {
+    const int g = threadIdx.x;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml_s[w][g].x);
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = ml_s[w][g];
+      const float c = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
+      if (ml.y != 0.f) L += c * ml.y;
+      cw_s[w][g] = c;
+    }
+    row_s[g] = make_float2(M, L);
+  }
+  named_barrier_sync(1, kWarps * 32);
+  const bool dead = bad_s != 0 || abort_s != 0;
+  ClusterXchg x;
+  if constexpr (CL) {
+    x = ClusterXchg(recv, R, D);
+    cluster_wait();
+  }
+  constexpr int kQuads = D / 4;
+  for (int e = threadIdx.x; e < R * kQuads; e += kWarps * 32) {
+    const int g = e / kQuads, q = e % kQuads;
+    const float2 ML = row_s[g];
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float c = cw_s[w][g];
+      if (c == 0.f) continue;
+      const float4 v = *reinterpret_cast<const float4*>(acc_s + (w * GP + g) * kRowStride + 4 * q);
+      O.x += c * v.x;
+      O.y += c * v.y;
+      O.z += c * v.z;
+      O.w += c * v.w;
+    }
+    const size_t row = group_row(b, h, g, a.T, a.G, a.Hq);
+    if (!a.split) {
+      if (!PGD_IN(row, (size_t)a.batch * a.T * a.Hq, a.err)) continue;
+      const bool z = dead || ML.y == 0.f;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 4 * q) = make_uint2(
+          ElemOps<E>::pack2(z ? 0.f : O.x / ML.y, z ? 0.f : O.y / ML.y),
+          ElemOps<E>::pack2(z ? 0.f : O.z / ML.y, z ? 0.f : O.w / ML.y));
+      continue;
+    }
+    const float4 Ow = dead ? make_float4(0.f, 0.f, 0.f, 0.f) : O;
+    const float2 MLw = make_float2(ML.x, dead ? -1.f : ML.y);
+    if constexpr (CL) {
+      x.push(e, Ow);
+      if (q == 0) x.push_ml(g, MLw);
+    } else {
+      const size_t slot = row * a.max_shards + s;
+      if (!PGD_IN(slot, (size_t)a.batch * a.T * a.Hq * a.max_shards, a.err)) continue;
+      *reinterpret_cast<float4*>(a.ws_acc + slot * D + 4 * q) = Ow;
+      if (q == 0) a.ws_ml[slot] = MLw;
+    }
+  }
+  if (!a.split) return;
+  if constexpr (CL)
+    cluster_finish<D, E>(a, x, b, h, smem_u32(&recv_bar), recv, kWarps * 32);
+  else
+    merge_if_last<D, E, 16>(a, r, b, h, ring, kWarps * 32);
+}
+
+}  // namespace pgd

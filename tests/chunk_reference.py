@@ -34,11 +34,13 @@ def cache_rows(pages, table_row, lo, hi, scales=None):
 
 def chunk_attention(q, k_pages, v_pages, table, off, lens, scale, window=0, k_scales=None,
                     v_scales=None):
-    """[total, Hq, D] in 64 bits: one exact softmax per row; a row without a
-    key is zero."""
+    """One exact softmax per row, in 64 bits; a row without a key is zero.
+    Returns (out, weighted): out [total, Hq, D], and the sum of p |v| beside
+    it, which bounds what an error of the weights does to an element."""
     Hq = q.shape[1]
     G = Hq // k_pages.shape[2]
     out = torch.zeros(q.shape, dtype=torch.float64)
+    mass = torch.zeros(q.shape, dtype=torch.float64)
     for b, L in enumerate(lens):
         L, a, z = int(L), int(off[b]), int(off[b + 1])
         n = z - a
@@ -54,16 +56,65 @@ def chunk_attention(q, k_pages, v_pages, table, off, lens, scale, window=0, k_sc
         if window > 0:
             hide = hide | (t <= p - window)
         s = s.masked_fill(hide, -math.inf)
+        top = s.amax(-1, keepdim=True)
         w = torch.where(hide, torch.zeros_like(s),
-                        torch.exp(s - s.amax(-1, keepdim=True).clamp(min=-1e300)))
+                        torch.exp(s - torch.where(top == -math.inf, torch.zeros_like(top), top)))
         tot = w.sum(-1, keepdim=True)
-        w = torch.where(tot > 0, w / tot.clamp(min=1e-300), torch.zeros_like(w))
-        # (a row outside the mask contributes nothing, whatever it holds)
-        o = torch.einsum("hnt,thd->nhd", w, torch.nan_to_num(V, nan=0.0, posinf=0.0, neginf=0.0))
-        out[a:z] = o
-    return out
+        w = torch.where(tot == 0, torch.zeros_like(w), w / tot)
+        out[a:z] = torch.einsum("hnt,thd->nhd", w, V)
+        mass[a:z] = torch.einsum("hnt,thd->nhd", w, V.abs())
+    return out, mass
+
+
+def score_size(q, k_pages, scale, k_scales=None):
+    """An upper bound of scale * sum_d |q_d k_d| over all rows (norms)."""
+    k = k_pages.view(torch.uint8).view(torch.float8_e4m3fn).double() if k_scales is not None \
+        else k_pages.double()
+    if k_scales is not None:
+        k = k * k_scales.transpose(1, 2).double()[..., None]
+    k = torch.nan_to_num(k, nan=0.0, posinf=0.0, neginf=0.0)
+    return float(abs(scale) * q.double().norm(dim=-1).max() * k.norm(dim=-1).max())
 
 
 def half_step(dtype):
     """Largest relative error of one rounding to `dtype`."""
     return torch.finfo(dtype).eps / 2
+
+
+def weight_error(D, size):
+    """Relative error of a softmax weight whose scores are summed in 32 bits:
+    D products in any order, each addition off by at most one step (the
+    tensor cores may cut where they add), twice over for the maximum and the
+    score, and the exponential (2^-22) with its argument's rounding."""
+    return 2 * D * 2.0 ** -23 * size + 2.0 ** -21 + 2 * size * 2.0 ** -23
+
+
+def assert_rows(got, out, mass, dtype, weight, tag=""):
+    """|got - out| at most: the weights' error on p |v|, once for the products
+    and once for their sum; two roundings of the result (the value itself, and
+    its division by the sum in 32 bits, 2^-23); the type's smallest step."""
+    g = got.double().cpu()
+    u = half_step(dtype)
+    tol = 2 * weight * mass + (u + 2.0 ** -22) * out.abs() + torch.finfo(dtype).smallest_normal * u
+    over = ((g - out).abs() - tol)
+    assert torch.isfinite(g).all(), tag
+    assert float(over.max()) <= 0, (tag, float(over.max()), float((g - out).abs().max()))
+
+
+def quantise(x):
+    """Rows [..., D] -> (e4m3 codes, scales [...]) from the definition: the
+    least power of two with max |x| <= 448 * scale (0 below 2^-100), the
+    nearest code, ties to even."""
+    x = x.double()
+    top = x.abs().amax(-1)
+    scale = torch.zeros_like(top)
+    flat, out = top.reshape(-1), scale.view(-1)
+    for i, t in enumerate(flat.tolist()):
+        if t >= 2.0 ** -100:
+            e = math.frexp(t)[1] - 9  # 2^(e + 8) <= t < 2^(e + 9)
+            if t > 448.0 * 2.0 ** e:
+                e += 1
+            out[i] = 2.0 ** e
+    y = torch.where(scale[..., None] > 0, x / scale.clamp(min=1e-300)[..., None],
+                    torch.zeros_like(x))
+    return y.float().to(torch.float8_e4m3fn), scale.float()
