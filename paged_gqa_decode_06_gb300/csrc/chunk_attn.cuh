@@ -154,13 +154,14 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   using C = ChunkCfg<D>;
   constexpr int NS = C::kStreams, KT = C::kKeys, NR = C::kRing;
   constexpr int kProducer = NS * 4, kMma = NS * 4 + 1;  // warps
+  constexpr int kParts = KT / 64;  // P is handed over 64 keys at a time
   constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
   constexpr uint32_t kIdescS = tc_idesc(128, KT, kBf16, false);
   constexpr uint32_t kIdescO = tc_idesc(128, D, kBf16, true);
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full, full_bar[NR], empty_bar[NR];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[NS], v_edge, v_clean;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2][kParts], o_full[NS], v_edge, v_clean;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int32_t abort_s;
   __shared__ int32_t bad_lo_s, bad_hi_s;  // positions in pages outside the pool
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
+      for (int k = 0; k < kParts; ++k) mbar_init(smem_u32(&p_full[i][k]), 4);
     }
     for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&o_full[i]), 1);
     mbar_init(smem_u32(&v_edge), 1);
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         if (r >= NR) {
           int go = 1;
           if (lane == 0) {
-            if (!mbar_wait(smem_u32(&empty_bar[slot_r]), ((r / NR) & 1) ^ 1)) {
+            if (!mbar_wait_hot(smem_u32(&empty_bar[slot_r]), ((r / NR) & 1) ^ 1)) {
               abort_s = 1;
               raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
             }
@@ -296,9 +297,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       // this CTA's copies in flight have landed before the warp exits
       if (lane == 0) {
-        mbar_wait(smem_u32(&q_full), 0);
+        mbar_wait_hot(smem_u32(&q_full), 0);
         for (int r = max(0, issued - NR); r < issued; ++r)
-          mbar_wait(smem_u32(&full_bar[r % NR]), (r / NR) & 1);
+          mbar_wait_hot(smem_u32(&full_bar[r % NR]), (r / NR) & 1);
       }
       return;
     }
@@ -311,25 +312,37 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       const uint32_t tmem = tmem_s, tmem_o = tmem + 2 * KT;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
-        if (ok && !mbar_wait(smem_u32(bar), parity)) {
+        if (ok && !mbar_wait_hot(smem_u32(bar), parity)) {
           abort_s = 1;
           raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+          ok = false;
         }
-        ok = __all_sync(0xffffffffu, ok && !abort_s);
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      const uint64_t qd = tc_desc(smem_u32(smem), 16, 1024);
+      const uint64_t kd = k_desc<D>(smem_u32(ring)), vd = v_desc<D>(smem_u32(ring));
+      constexpr uint32_t kTile16 = C::kTileBytes / 16;
+      int told = 0, cleaned = 0;  // edge tiles handed over for a look at V, and used
+      int next = 0;               // first tile whose V has not been waited for or handed over
+      auto hand_over = [&](int j) {
+        if (edge(j)) {
+          if (lane == 0) mbar_arrive(smem_u32(&v_edge));
+          ++told;
+        }
+        next = j + 1;
       };
       auto issue_s = [&](int u) {  // S(u) = Q . K^T
         const int j = u / ns, s = u % ns, r = 2 * j;
         if (s == 0) wait(&full_bar[r % NR], (r / NR) & 1);
         if (!ok) return;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
-          const uint64_t qd = tc_desc(smem_u32(smem + s * C::kQBytes), 16, 1024);
-          const uint64_t kd = k_desc<D>(smem_u32(ring + (r % NR) * C::kTileBytes));
+          const uint64_t q0 = qd + s * (C::kQBytes / 16), k0 = kd + (r % NR) * kTile16;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const int c = ks >> 2, in = (ks & 3) * 2;  // 32 bytes inside a 64-dim chunk
-            tc_mma_ss(tmem + (u & 1) * KT, qd + c * (128 * 128 / 16) + in, kd + c * (1024 / 16) + in,
-                      kIdescS, ks > 0);
+            tc_mma_ss(tmem + (u & 1) * KT, q0 + c * (128 * 128 / 16) + in,
+                      k0 + c * (1024 / 16) + in, kIdescS, ks > 0);
           }
           tc_commit(smem_u32(&s_full[u & 1]));
           if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
@@ -339,29 +352,39 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       wait(&q_full, 0);
       issue_s(0);
       if (units > 1) issue_s(1);
-      int edges = 0;
       for (int u = 0; u < units && ok; ++u) {
         const int j = u / ns, s = u % ns, r = 2 * j + 1;
-        uint8_t* vt = ring + (r % NR) * C::kTileBytes;
-        if (s == 0) {
+        if (s == 0 && next <= j) {
           wait(&full_bar[r % NR], (r / NR) & 1);
-          if (ok && edge(j) && lane == 0) mbar_arrive(smem_u32(&v_edge));
+          if (ok) hand_over(j);
         }
-        wait(&p_full[u & 1], (u >> 1) & 1);
-        if (s == 0 && edge(j)) wait(&v_clean, edges++ & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t vd = v_desc<D>(smem_u32(vt));
+        for (int part = 0; part < kParts; ++part) {
+          wait(&p_full[u & 1][part], (u >> 1) & 1);
+          if (part == 0 && s == 0 && edge(j)) wait(&v_clean, cleaned++ & 1);
+          if (!ok) break;
+          if (elect_one()) {
+            tc_fence_after();
+            const uint64_t v0 = vd + (r % NR) * kTile16 + part * (64 * D * 2 / 16);
+            const uint32_t p0 = tmem + (u & 1) * KT + part * 32;
 #pragma unroll
-          for (int ks = 0; ks < KT / 16; ++ks)  // O += P . V
-            tc_mma_ts(tmem_o + s * D, tmem + (u & 1) * KT + ks * 8, vd + ks * (D * 32 / 16), kIdescO,
-                      j > 0 || ks > 0);
-          tc_commit(smem_u32(&o_full[s]));
-          if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
+            for (int ks = 0; ks < 4; ++ks)  // O += P . V, 64 keys
+              tc_mma_ts(tmem_o + s * D, p0 + ks * 8, v0 + ks * (D * 32 / 16), kIdescO,
+                        j > 0 || part > 0 || ks > 0);
+            if (part == kParts - 1) {
+              tc_commit(smem_u32(&o_full[s]));
+              if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
         if (u + 2 < units) issue_s(u + 2);
+        // V of the next tile, if it has come already: an edge tile is looked
+        // over while this tile's weights are made
+        if (ok && next <= j + 1 && j + 1 < ntiles &&
+            __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full_bar[(r + 2) % NR]),
+                                                  ((r + 2) / NR) & 1)))
+          hand_over(j + 1);
       }
       named_barrier_sync(1, kOthers);  // every row has been read out
       tc_fence_after();
@@ -372,13 +395,24 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     int edges = 0;
     for (int j = 0; j < ntiles; ++j) {
       if (!edge(j)) continue;
-      if (!mbar_wait(smem_u32(&v_edge), edges & 1)) abort_s = 1;
+      if (!mbar_wait_hot(smem_u32(&v_edge), edges & 1)) abort_s = 1;
       if (!__all_sync(0xffffffffu, !abort_s)) break;
       const int k0 = key0 + j * KT;
       uint8_t* vt = ring + ((2 * j + 1) % NR) * C::kTileBytes;
       if (warp == kMma + 1 && lane == 0 && edges < C::kMaxEdges) edge_key_s[edges] = k0;
-#pragma unroll 4
-      for (int e = (warp - kMma - 1) * 32 + lane; e < C::kTileBytes / 16; e += 64) {
+      // a quick pass: whether any value of the tile needs a look at all
+      const int first = (warp - kMma - 1) * 32 + lane;
+      bool look = k0 < it.lo || k0 + KT > it.hi;
+      if (!look) {
+        uint32_t any = 0;
+#pragma unroll 8
+        for (int e = first; e < C::kTileBytes / 16; e += 64) {
+          const uint4 v = reinterpret_cast<const uint4*>(vt)[e];
+          any |= wild2<E>(v.x) | wild2<E>(v.y) | wild2<E>(v.z) | wild2<E>(v.w);
+        }
+        look = any != 0;
+      }
+      for (int e = first; look && e < C::kTileBytes / 16; e += 64) {
         const int t = e / D * 8 + (e % 64) / 8;  // groups of 8 tokens, 1 KB per 64 dims
         uint4* at = reinterpret_cast<uint4*>(vt) + e;
         if (k0 + t < it.lo || k0 + t >= it.hi) {
@@ -422,11 +456,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     for (int j = 0; j < ntiles; ++j) {
       const int u = j * ns + s, buf = u & 1;
       const uint32_t tm_s = tmem + buf * KT + lanes;
-      if (!mbar_wait(smem_u32(&s_full[buf]), (u >> 1) & 1)) {
+      if (!mbar_wait_hot(smem_u32(&s_full[buf]), (u >> 1) & 1)) {
         abort_s = 1;
         raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+        ok = false;
       }
-      ok = __all_sync(0xffffffffu, !abort_s);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       float x[KT];
@@ -447,13 +482,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         for (int i = 0; i < KT; ++i) x[i] = (i <= top && i > bottom) ? x[i] * mult : -INFINITY;
         mult = 1.f;
       }
-      float mx0 = max3(x[0], x[1], x[2]), mx1 = x[3];
+      float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
       for (int i = 4; i < KT; i += 4) {
-        mx0 = max3(mx0, x[i], x[i + 1]);
-        mx1 = max3(mx1, x[i + 2], x[i + 3]);
+        top[(i >> 2) & 1] = max3(top[(i >> 2) & 1], x[i], x[i + 1]);
+        top[2 + ((i >> 2) & 1)] = max3(top[2 + ((i >> 2) & 1)], x[i + 2], x[i + 3]);
       }
-      const float mx = fmaxf(mx0, mx1) * mult;
+      const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * mult;
       // The reference maximum follows only when it would grow by more than
       // 2^8: the weights stay below that, and the accumulator is rescaled
       // for a few tiles instead of nearly every one.
@@ -464,7 +499,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O holds the products up to the unit before: rescale it in place
-        if (!mbar_wait(smem_u32(&o_full[s]), (j - 1) & 1)) {
+        if (!mbar_wait_hot(smem_u32(&o_full[s]), (j - 1) & 1)) {
           abort_s = 1;
           raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
         }
@@ -488,30 +523,33 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       const float mu = m == -INFINITY ? 0.f : m;  // a row without a key so far
       const uint64_t mult2 = pair(mult, mult), nm2 = pair(-mu, -mu);
 #pragma unroll
-      for (int c = 0; c < KT; c += 64) {
+      for (int part = 0; part < kParts; ++part) {
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float2 e = unpair(fma2(pair(x[c + 2 * i], x[c + 2 * i + 1]), mult2, nm2));
+          const int k = part * 64 + 2 * i;
+          const float2 e = unpair(fma2(pair(x[k], x[k + 1]), mult2, nm2));
           const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
           l2 = add2(l2, pair(p0, p1));
           w[i] = ElemOps<E>::pack2(p0, p1);
         }
-        tmem_st32(tm_s + c / 2, w);
+        tmem_st32(tm_s + part * 32, w);
+        tmem_wait_st();
+        // A parity tells only two neighbouring phases apart: before the last
+        // weights go out, the product before theirs is known to be done (it
+        // is, but for a single stream's), so that the wait after the loop
+        // means the last one.
+        if (part == 0 && j == ntiles - 1 && j > 0 &&
+            !mbar_wait_hot(smem_u32(&o_full[s]), (j - 1) & 1)) {
+          abort_s = 1;
+          raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[buf][part]));
       }
-      tmem_wait_st();
-      // A parity tells only two neighbouring phases apart: before the last
-      // weights go out, the product before theirs is known to be done (it is,
-      // but for a single stream's), so that the wait below means the last one.
-      if (j == ntiles - 1 && j > 0 && !mbar_wait(smem_u32(&o_full[s]), (j - 1) & 1)) {
-        abort_s = 1;
-        raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
     }
-    if (ok && !mbar_wait(smem_u32(&o_full[s]), (ntiles - 1) & 1)) {
+    if (ok && !mbar_wait_hot(smem_u32(&o_full[s]), (ntiles - 1) & 1)) {
       abort_s = 1;
       raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
     }

@@ -9,6 +9,22 @@
 
 namespace pgd {
 
+// mbar_wait for waits in a pipeline's inner loop: the clock is read once in
+// 1024 tries only, since a read between two tries delays the wake-up (a
+// prompt of 8192 tokens with it in every turn: see chunk_attn.cuh).  Gives up
+// after about two seconds as mbar_wait does.
+__device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 0) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > 2000000000ull) return false;
+    }
+  }
+}
+
 // Tensor memory: `ncols` (a power of two, at least 32) columns of 128 lanes,
 // allocated by one whole warp; the address lands in shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t ncols) {
@@ -20,6 +36,17 @@ __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t ncols) {
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(ncols)
                : "memory");
+}
+
+// True in one lane of a converged warp.  Around matrix instructions this and
+// not `lane == 0`: the compiler then knows that one thread runs them and
+// keeps their descriptors in uniform registers (8 instructions of 128 x 128 x
+// 16 in a row: about 600 cycles against 780).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e != 0;
 }
 
 __device__ __forceinline__ void tc_fence_before() {
