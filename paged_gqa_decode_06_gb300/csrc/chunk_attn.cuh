@@ -72,6 +72,7 @@ struct ChunkCfg {
   static constexpr int kStreams = D <= 128 ? 2 : 1;
   static constexpr int kKeys = D <= 128 ? 128 : 64;  // keys of one tile
   static constexpr int kThreads = kStreams * 128 + 128;
+  static constexpr int kParts = kKeys / 64;  // P is handed over 64 keys at a time
   static constexpr int kTileBytes = kKeys * D * 2;
   static constexpr int kQBytes = 128 * D * 2;  // one stream
   // the ring holds K and V tiles in turn
@@ -81,6 +82,18 @@ struct ChunkCfg {
   // edge tiles of one CTA: the diagonal and a window's start each cross at
   // most 3 tiles (256 tokens, 128 at D = 256)
   static constexpr int kMaxEdges = 8;
+};
+
+// The barriers of a CTA's pipeline.
+template <int D>
+struct __align__(8) ChunkBars {
+  uint64_t q_full;                        // Q has landed
+  uint64_t full[ChunkCfg<D>::kRing];      // a K or V tile has landed
+  uint64_t empty[ChunkCfg<D>::kRing];     // the products are done with it
+  uint64_t s_full[2];                     // scores of a unit are in tensor memory
+  uint64_t p_full[2][ChunkCfg<D>::kParts];  // so are its weights, 64 keys each
+  uint64_t o_full[ChunkCfg<D>::kStreams];   // a unit's product is in O
+  uint64_t v_edge, v_clean;               // an edge tile's V has landed; is looked over
 };
 
 // One CTA's share of the work, found from its slot.
@@ -146,6 +159,112 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t tile) {
   return tc_desc(tile, 1024, D * 16);
 }
 
+// A tile's place in the ring: K and V tiles alternate, so the next one of
+// either is two places on.
+template <int NR>
+struct RingPos {
+  int slot, phase;
+  __device__ void next() {
+    slot += 2;
+    if (slot >= NR) {
+      slot -= NR;
+      phase ^= 1;
+    }
+  }
+};
+
+// Waits for and issues every product of the CTA, in one thread: the pace of
+// this loop is the pace of the tensor cores.  NA streams are active; unit u
+// is (tile u / NA, stream u % NA) and uses S buffer u % 2.
+template <int D, class E, int NA, class Edge>
+__device__ __forceinline__ void chunk_issue(ChunkBars<D>& bar, uint8_t* smem, uint32_t tmem,
+                                            int ntiles, Edge edge, volatile int32_t* abort_s,
+                                            const ChunkArgs& a) {
+  using C = ChunkCfg<D>;
+  constexpr int KT = C::kKeys, NR = C::kRing;
+  constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
+  constexpr uint32_t kIdescS = tc_idesc(128, KT, kBf16, false);
+  constexpr uint32_t kIdescO = tc_idesc(128, D, kBf16, true);
+  constexpr uint32_t kTile16 = C::kTileBytes / 16;
+  const uint64_t qd = tc_desc(smem_u32(smem), 16, 1024);
+  const uint64_t kd = k_desc<D>(smem_u32(smem + C::kStreams * C::kQBytes));
+  const uint64_t vd = v_desc<D>(smem_u32(smem + C::kStreams * C::kQBytes));
+  const uint32_t tmem_o = tmem + 2 * KT;
+  bool ok = true;
+  auto wait = [&](uint64_t* b, int parity) {
+    if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
+      *abort_s = 1;
+      raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
+      ok = false;
+    }
+  };
+  RingPos<NR> kp{0, 0}, vp{1, 0};
+  // S = Q . K^T of stream s and the tile at kp, into buffer buf
+  auto issue_s = [&](int s, int buf) {
+    if (s == 0) wait(&bar.full[kp.slot], kp.phase);
+    if (!ok) return;
+    tc_fence_after();
+    const uint64_t q0 = qd + s * (C::kQBytes / 16), k0 = kd + kp.slot * kTile16;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const int c = ks >> 2, in = (ks & 3) * 2;  // 32 bytes inside a 64-dim chunk
+      tc_mma_ss(tmem + buf * KT, q0 + c * (128 * 128 / 16) + in, k0 + c * (1024 / 16) + in,
+                kIdescS, ks > 0);
+    }
+    tc_commit(smem_u32(&bar.s_full[buf]));
+    if (s == NA - 1) {
+      tc_commit(smem_u32(&bar.empty[kp.slot]));
+      kp.next();
+    }
+  };
+  wait(&bar.q_full, 0);
+  issue_s(0, 0);
+  if (NA == 2)
+    issue_s(1, 1);
+  else if (ntiles > 1)
+    issue_s(0, 1);
+  int cleaned = 0;        // edge tiles looked over so far
+  bool told = false;      // V of this tile has landed and, an edge tile's, been handed over
+  for (int j = 0; j < ntiles && ok; ++j) {
+    const bool is_edge = edge(j);
+    if (!told) {
+      wait(&bar.full[vp.slot], vp.phase);
+      if (is_edge) mbar_arrive(smem_u32(&bar.v_edge));
+    }
+    told = false;
+#pragma unroll
+    for (int s = 0; s < NA; ++s) {
+      const int buf = NA == 2 ? s : (j & 1), phase = NA == 2 ? (j & 1) : ((j >> 1) & 1);
+#pragma unroll
+      for (int part = 0; part < C::kParts; ++part) {
+        wait(&bar.p_full[buf][part], phase);
+        if (part == 0 && s == 0 && is_edge) wait(&bar.v_clean, cleaned++ & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t v0 = vd + vp.slot * kTile16 + part * (64 * D * 2 / 16);
+        const uint32_t p0 = tmem + buf * KT + part * 32;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)  // O += P . V, 64 keys
+          tc_mma_ts(tmem_o + s * D, p0 + ks * 8, v0 + ks * (D * 32 / 16), kIdescO,
+                    j > 0 || part > 0 || ks > 0);
+      }
+      tc_commit(smem_u32(&bar.o_full[s]));
+      if (s == NA - 1) {
+        tc_commit(smem_u32(&bar.empty[vp.slot]));
+        vp.next();
+      }
+      if (j + (NA == 2 ? 1 : 2) < ntiles) issue_s(s, buf);
+    }
+    // an edge tile whose V has come already is handed over now, and looked
+    // over while its weights are made
+    if (j + 1 < ntiles && edge(j + 1) &&
+        mbar_try_wait(smem_u32(&bar.full[vp.slot]), vp.phase)) {
+      mbar_arrive(smem_u32(&bar.v_edge));
+      told = true;
+    }
+  }
+}
+
 template <int D, class E>
 __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -154,14 +273,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   using C = ChunkCfg<D>;
   constexpr int NS = C::kStreams, KT = C::kKeys, NR = C::kRing;
   constexpr int kProducer = NS * 4, kMma = NS * 4 + 1;  // warps
-  constexpr int kParts = KT / 64;  // P is handed over 64 keys at a time
-  constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
-  constexpr uint32_t kIdescS = tc_idesc(128, KT, kBf16, false);
-  constexpr uint32_t kIdescO = tc_idesc(128, D, kBf16, true);
+  constexpr int kParts = C::kParts;
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full, full_bar[NR], empty_bar[NR];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2][kParts], o_full[NS], v_edge, v_clean;
+  __shared__ ChunkBars<D> bar;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int32_t abort_s;
   __shared__ int32_t bad_lo_s, bad_hi_s;  // positions in pages outside the pool
@@ -178,18 +293,18 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     prefetch_tensormap(&tmap_q);
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
-    mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&bar.q_full), 1);
     for (int i = 0; i < NR; ++i) {
-      mbar_init(smem_u32(&full_bar[i]), 1);
-      mbar_init(smem_u32(&empty_bar[i]), 1);
+      mbar_init(smem_u32(&bar.full[i]), 1);
+      mbar_init(smem_u32(&bar.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s_full[i]), 1);
-      for (int k = 0; k < kParts; ++k) mbar_init(smem_u32(&p_full[i][k]), 4);
+      mbar_init(smem_u32(&bar.s_full[i]), 1);
+      for (int k = 0; k < kParts; ++k) mbar_init(smem_u32(&bar.p_full[i][k]), 4);
     }
-    for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&o_full[i]), 1);
-    mbar_init(smem_u32(&v_edge), 1);
-    mbar_init(smem_u32(&v_clean), 2);
+    for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&bar.o_full[i]), 1);
+    mbar_init(smem_u32(&bar.v_edge), 1);
+    mbar_init(smem_u32(&bar.v_clean), 2);
     fence_mbar_init();
     abort_s = 0;
     bad_lo_s = INT32_MAX;
@@ -229,7 +344,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const int ntiles = (int)((int64_t)it.tiles * (shard + 1) / it.shards) - tile0;
   const int key0 = it.base + tile0 * KT;  // first key of this CTA's first tile
   const int ns = (it.t1 - it.t0) > a.tile_tok ? NS : 1;  // streams with tokens
-  const int units = ntiles * ns;
   // whether some row of the CTA does not attend all of tile j
   const int plast = it.p0 + (it.t1 - it.t0) - 1;
   auto edge = [&](int j) {
@@ -238,13 +352,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   };
 
   // two streams: 384 threads launched with 168 registers each; the row
-  // threads (a row of 128 scores apiece) take 224, the last warpgroup 56
+  // threads (a row of 128 scores apiece) take 208, the last warpgroup 88
   constexpr int kOthers = NS * 128 + 32;  // the row threads and the issuing warp
   if (warp >= kProducer) {
-    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kProducer) {
       if (lane == 0) {
-        const uint32_t qb = smem_u32(&q_full);
+        const uint32_t qb = smem_u32(&bar.q_full);
         mbar_arrive_expect_tx(qb, (uint32_t)(ns * (D / 64) * a.tile_tok * a.G * 128));
         for (int s = 0; s < ns; ++s)
           for (int c = 0; c < D / 64; ++c)
@@ -279,7 +393,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         if (r >= NR) {
           int go = 1;
           if (lane == 0) {
-            if (!mbar_wait_hot(smem_u32(&empty_bar[slot_r]), ((r / NR) & 1) ^ 1)) {
+            if (!mbar_wait_hot(smem_u32(&bar.empty[slot_r]), ((r / NR) & 1) ^ 1)) {
               abort_s = 1;
               raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
             }
@@ -287,7 +401,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) break;
         }
-        const uint32_t fb = smem_u32(&full_bar[slot_r]);
+        const uint32_t fb = smem_u32(&bar.full[slot_r]);
         if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes + (r == 0 ? a.stall_tx : 0));
         __syncwarp();
         if (lane < pieces)
@@ -297,9 +411,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       // this CTA's copies in flight have landed before the warp exits
       if (lane == 0) {
-        mbar_wait_hot(smem_u32(&q_full), 0);
+        mbar_wait_hot(smem_u32(&bar.q_full), 0);
         for (int r = max(0, issued - NR); r < issued; ++r)
-          mbar_wait_hot(smem_u32(&full_bar[r % NR]), (r / NR) & 1);
+          mbar_wait_hot(smem_u32(&bar.full[r % NR]), (r / NR) & 1);
       }
       return;
     }
@@ -309,93 +423,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       tc_fence_before();
       named_barrier_sync(1, kOthers);
       tc_fence_after();
-      const uint32_t tmem = tmem_s, tmem_o = tmem + 2 * KT;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, int parity) {
-        if (ok && !mbar_wait_hot(smem_u32(bar), parity)) {
-          abort_s = 1;
-          raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
-          ok = false;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-      };
-      const uint64_t qd = tc_desc(smem_u32(smem), 16, 1024);
-      const uint64_t kd = k_desc<D>(smem_u32(ring)), vd = v_desc<D>(smem_u32(ring));
-      constexpr uint32_t kTile16 = C::kTileBytes / 16;
-      int told = 0, cleaned = 0;  // edge tiles handed over for a look at V, and used
-      int next = 0;               // first tile whose V has not been waited for or handed over
-      auto hand_over = [&](int j) {
-        if (edge(j)) {
-          if (lane == 0) mbar_arrive(smem_u32(&v_edge));
-          ++told;
-        }
-        next = j + 1;
-      };
-      auto issue_s = [&](int u) {  // S(u) = Q . K^T
-        const int j = u / ns, s = u % ns, r = 2 * j;
-        if (s == 0) wait(&full_bar[r % NR], (r / NR) & 1);
-        if (!ok) return;
-        if (elect_one()) {
-          tc_fence_after();
-          const uint64_t q0 = qd + s * (C::kQBytes / 16), k0 = kd + (r % NR) * kTile16;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const int c = ks >> 2, in = (ks & 3) * 2;  // 32 bytes inside a 64-dim chunk
-            tc_mma_ss(tmem + (u & 1) * KT, q0 + c * (128 * 128 / 16) + in,
-                      k0 + c * (1024 / 16) + in, kIdescS, ks > 0);
-          }
-          tc_commit(smem_u32(&s_full[u & 1]));
-          if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
-        }
-        __syncwarp();
-      };
-      wait(&q_full, 0);
-      issue_s(0);
-      if (units > 1) issue_s(1);
-      for (int u = 0; u < units && ok; ++u) {
-        const int j = u / ns, s = u % ns, r = 2 * j + 1;
-        if (s == 0 && next <= j) {
-          wait(&full_bar[r % NR], (r / NR) & 1);
-          if (ok) hand_over(j);
-        }
-        for (int part = 0; part < kParts; ++part) {
-          wait(&p_full[u & 1][part], (u >> 1) & 1);
-          if (part == 0 && s == 0 && edge(j)) wait(&v_clean, cleaned++ & 1);
-          if (!ok) break;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t v0 = vd + (r % NR) * kTile16 + part * (64 * D * 2 / 16);
-            const uint32_t p0 = tmem + (u & 1) * KT + part * 32;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // O += P . V, 64 keys
-              tc_mma_ts(tmem_o + s * D, p0 + ks * 8, v0 + ks * (D * 32 / 16), kIdescO,
-                        j > 0 || part > 0 || ks > 0);
-            if (part == kParts - 1) {
-              tc_commit(smem_u32(&o_full[s]));
-              if (s == ns - 1) tc_commit(smem_u32(&empty_bar[r % NR]));
-            }
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (u + 2 < units) issue_s(u + 2);
-        // V of the next tile, if it has come already: an edge tile is looked
-        // over while this tile's weights are made
-        if (ok && next <= j + 1 && j + 1 < ntiles &&
-            __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full_bar[(r + 2) % NR]),
-                                                  ((r + 2) / NR) & 1)))
-          hand_over(j + 1);
+      // One thread waits for and issues everything: the pace of this loop is
+      // the pace of the tensor cores (with warp-wide waits and votes a unit
+      // took 2000 cycles, of which the products need 1100).
+      if (elect_one()) {
+        if (NS == 2 && ns == 2)
+          chunk_issue<D, E, NS>(bar, smem, tmem_s, ntiles, edge, &abort_s, a);
+        else
+          chunk_issue<D, E, 1>(bar, smem, tmem_s, ntiles, edge, &abort_s, a);
       }
+      __syncwarp();
       named_barrier_sync(1, kOthers);  // every row has been read out
       tc_fence_after();
-      tmem_free(tmem, C::kTmemCols);
+      tmem_free(tmem_s, C::kTmemCols);
       return;
     }
     // the two warps that look over V's edge tiles
     int edges = 0;
     for (int j = 0; j < ntiles; ++j) {
       if (!edge(j)) continue;
-      if (!mbar_wait_hot(smem_u32(&v_edge), edges & 1)) abort_s = 1;
+      if (!mbar_wait_hot(smem_u32(&bar.v_edge), edges & 1)) abort_s = 1;
       if (!__all_sync(0xffffffffu, !abort_s)) break;
       const int k0 = key0 + j * KT;
       uint8_t* vt = ring + ((2 * j + 1) % NR) * C::kTileBytes;
@@ -428,14 +475,14 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&v_clean));
+      if (lane == 0) mbar_arrive(smem_u32(&bar.v_clean));
       ++edges;
     }
     return;
   }
 
   // ---------------------------------------------------------- softmax rows
-  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   named_barrier_sync(1, kOthers);  // the tensor memory is there
   tc_fence_after();
   const uint32_t tmem = tmem_s, tmem_o = tmem + 2 * KT;  // O after the two S buffers
@@ -456,7 +503,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     for (int j = 0; j < ntiles; ++j) {
       const int u = j * ns + s, buf = u & 1;
       const uint32_t tm_s = tmem + buf * KT + lanes;
-      if (!mbar_wait_hot(smem_u32(&s_full[buf]), (u >> 1) & 1)) {
+      if (!mbar_wait_hot(smem_u32(&bar.s_full[buf]), (u >> 1) & 1)) {
         abort_s = 1;
         raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
         ok = false;
@@ -499,7 +546,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O holds the products up to the unit before: rescale it in place
-        if (!mbar_wait_hot(smem_u32(&o_full[s]), (j - 1) & 1)) {
+        if (!mbar_wait_hot(smem_u32(&bar.o_full[s]), (j - 1) & 1)) {
           abort_s = 1;
           raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
         }
@@ -511,13 +558,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         const uint64_t al = pair(alpha, alpha);
         l2 = mul2(l2, al);
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(o, tmem_o + s * D + lanes + c);
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tmem_ld16(o, tmem_o + s * D + lanes + c);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(tmem_o + s * D + lanes + c, reinterpret_cast<const uint32_t*>(o));
+          for (int i = 0; i < 16; ++i) o[i] *= alpha;
+          tmem_st16(tmem_o + s * D + lanes + c, reinterpret_cast<const uint32_t*>(o));
         }
       }
       const float mu = m == -INFINITY ? 0.f : m;  // a row without a key so far
@@ -540,16 +587,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         // is, but for a single stream's), so that the wait after the loop
         // means the last one.
         if (part == 0 && j == ntiles - 1 && j > 0 &&
-            !mbar_wait_hot(smem_u32(&o_full[s]), (j - 1) & 1)) {
+            !mbar_wait_hot(smem_u32(&bar.o_full[s]), (j - 1) & 1)) {
           abort_s = 1;
           raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[buf][part]));
+        if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[buf][part]));
       }
     }
-    if (ok && !mbar_wait_hot(smem_u32(&o_full[s]), (ntiles - 1) & 1)) {
+    if (ok && !mbar_wait_hot(smem_u32(&bar.o_full[s]), (ntiles - 1) & 1)) {
       abort_s = 1;
       raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
     }
