@@ -67,6 +67,31 @@ struct ChunkArgs {
   float scale_log2;
 };
 
+// The barriers of a CTA's pipeline: kRing tiles of K and V, kStreams streams.
+template <int kRing, int kStreams, int kParts>
+struct __align__(8) ChunkBars {
+  uint64_t q_full;            // Q has landed
+  uint64_t full[kRing];       // a K or V tile has landed
+  uint64_t empty[kRing];      // the products are done with it
+  uint64_t s_full[2];         // scores of a unit are in tensor memory
+  uint64_t p_full[2][kParts]; // so are its weights, 64 keys each
+  uint64_t o_full[kStreams];  // a unit's product is in O
+  uint64_t done[kStreams];    // so is the last one's
+  uint64_t v_edge, v_clean;   // an edge tile's V has landed; is looked over
+};
+
+// What the CTA shares beside Q and the ring.
+template <int kRing, int kStreams, int kKeys, int kMaxEdges>
+struct ChunkShared {
+  ChunkBars<kRing, kStreams, kKeys / 64> bar;
+  uint32_t tmem;
+  int32_t abort;
+  int32_t bad_lo, bad_hi;  // positions in pages outside the pool
+  // keys of the edge tiles whose V row is not finite
+  uint32_t wild[kMaxEdges][kKeys / 32];
+  int32_t edge_key[kMaxEdges], wild_any;
+};
+
 template <int D>
 struct ChunkCfg {
   static constexpr int kStreams = D <= 128 ? 2 : 1;
@@ -77,23 +102,14 @@ struct ChunkCfg {
   static constexpr int kQBytes = 128 * D * 2;  // one stream
   // the ring holds K and V tiles in turn
   static constexpr int kRing = D == 64 ? 8 : 5;
-  static constexpr int kSmemBytes = kStreams * kQBytes + kRing * kTileBytes + 1024;
   static constexpr uint32_t kTmemCols = 512;
   // edge tiles of one CTA: the diagonal and a window's start each cross at
   // most 3 tiles (256 tokens, 128 at D = 256)
   static constexpr int kMaxEdges = 8;
-};
-
-// The barriers of a CTA's pipeline.
-template <int D>
-struct __align__(8) ChunkBars {
-  uint64_t q_full;                        // Q has landed
-  uint64_t full[ChunkCfg<D>::kRing];      // a K or V tile has landed
-  uint64_t empty[ChunkCfg<D>::kRing];     // the products are done with it
-  uint64_t s_full[2];                     // scores of a unit are in tensor memory
-  uint64_t p_full[2][ChunkCfg<D>::kParts];  // so are its weights, 64 keys each
-  uint64_t o_full[ChunkCfg<D>::kStreams];   // a unit's product is in O
-  uint64_t v_edge, v_clean;               // an edge tile's V has landed; is looked over
+  using Bars = ChunkBars<kRing, kStreams, kParts>;
+  using Shared = ChunkShared<kRing, kStreams, kKeys, kMaxEdges>;
+  static constexpr int kSmemBytes = kStreams * kQBytes + kRing * kTileBytes + sizeof(Shared);
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 };
 
 // One CTA's share of the work, found from its slot.
@@ -150,6 +166,11 @@ __device__ __forceinline__ uint32_t wild2(uint32_t w) {
   return __vcmpeq2(w & kExp, kExp);
 }
 
+// The lowest n bits, for any n.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : 0xffffffffu >> (32 - min(n, 32));
+}
+
 template <int D>
 __device__ __forceinline__ uint64_t k_desc(uint32_t tile) {
   return tc_desc(tile, 16, D * 16);
@@ -177,13 +198,15 @@ struct RingPos {
 // this loop is the pace of the tensor cores.  NA streams are active; unit u
 // is (tile u / NA, stream u % NA) and uses S buffer u % 2.
 template <int D, class E, int NA, class Edge>
-__device__ __forceinline__ void chunk_issue(ChunkBars<D>& bar, uint8_t* smem, uint32_t tmem,
-                                            int ntiles, Edge edge, volatile int32_t* abort_s,
-                                            const ChunkArgs& a) {
+__device__ __forceinline__ void chunk_issue(typename ChunkCfg<D>::Bars& bar, uint8_t* smem,
+                                            uint32_t tmem, int ntiles, Edge edge,
+                                            volatile int32_t* abort, const ChunkArgs& a) {
   using C = ChunkCfg<D>;
   constexpr int KT = C::kKeys, NR = C::kRing;
   constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
-  constexpr uint32_t kIdescS = tc_idesc(128, KT, kBf16, false);
+  // a negative scale turns the scores' sign here, so that the softmax only
+  // sees its magnitude
+  const uint32_t idesc_s = tc_idesc(128, KT, kBf16, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
   constexpr uint32_t kIdescO = tc_idesc(128, D, kBf16, true);
   constexpr uint32_t kTile16 = C::kTileBytes / 16;
   const uint64_t qd = tc_desc(smem_u32(smem), 16, 1024);
@@ -193,7 +216,7 @@ __device__ __forceinline__ void chunk_issue(ChunkBars<D>& bar, uint8_t* smem, ui
   bool ok = true;
   auto wait = [&](uint64_t* b, int parity) {
     if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
-      *abort_s = 1;
+      *abort = 1;
       raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
       ok = false;
     }
@@ -209,7 +232,7 @@ __device__ __forceinline__ void chunk_issue(ChunkBars<D>& bar, uint8_t* smem, ui
     for (int ks = 0; ks < D / 16; ++ks) {
       const int c = ks >> 2, in = (ks & 3) * 2;  // 32 bytes inside a 64-dim chunk
       tc_mma_ss(tmem + buf * KT, q0 + c * (128 * 128 / 16) + in, k0 + c * (1024 / 16) + in,
-                kIdescS, ks > 0);
+                idesc_s, ks > 0);
     }
     tc_commit(smem_u32(&bar.s_full[buf]));
     if (s == NA - 1) {
@@ -249,6 +272,7 @@ __device__ __forceinline__ void chunk_issue(ChunkBars<D>& bar, uint8_t* smem, ui
                     j > 0 || part > 0 || ks > 0);
       }
       tc_commit(smem_u32(&bar.o_full[s]));
+      if (j == ntiles - 1) tc_commit(smem_u32(&bar.done[s]));
       if (s == NA - 1) {
         tc_commit(smem_u32(&bar.empty[vp.slot]));
         vp.next();
@@ -273,20 +297,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   using C = ChunkCfg<D>;
   constexpr int NS = C::kStreams, KT = C::kKeys, NR = C::kRing;
   constexpr int kProducer = NS * 4, kMma = NS * 4 + 1;  // warps
-  constexpr int kParts = C::kParts;
 
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ ChunkBars<D> bar;
-  __shared__ uint32_t tmem_s;
-  __shared__ volatile int32_t abort_s;
-  __shared__ int32_t bad_lo_s, bad_hi_s;  // positions in pages outside the pool
-  // keys of the edge tiles whose V row is not finite
-  __shared__ uint32_t wild_s[C::kMaxEdges][KT / 32];
-  __shared__ int32_t edge_key_s[C::kMaxEdges], wild_any_s;
-
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + NS * C::kQBytes;
+  typename C::Shared& sh = *reinterpret_cast<typename C::Shared*>(ring + NR * C::kTileBytes);
+  typename C::Bars& bar = sh.bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == kProducer * 32) {
@@ -300,19 +315,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bar.s_full[i]), 1);
-      for (int k = 0; k < kParts; ++k) mbar_init(smem_u32(&bar.p_full[i][k]), 4);
+      for (int k = 0; k < C::kParts; ++k) mbar_init(smem_u32(&bar.p_full[i][k]), 4);
     }
-    for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&bar.o_full[i]), 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&bar.o_full[i]), 1);
+      mbar_init(smem_u32(&bar.done[i]), 1);
+    }
     mbar_init(smem_u32(&bar.v_edge), 1);
     mbar_init(smem_u32(&bar.v_clean), 2);
     fence_mbar_init();
-    abort_s = 0;
-    bad_lo_s = INT32_MAX;
-    bad_hi_s = -1;
-    wild_any_s = 0;
+    sh.abort = 0;
+    sh.bad_lo = INT32_MAX;
+    sh.bad_hi = -1;
+    sh.wild_any = 0;
   }
   for (int i = threadIdx.x; i < C::kMaxEdges * KT / 32; i += C::kThreads)
-    wild_s[i / (KT / 32)][i % (KT / 32)] = 0u;
+    sh.wild[i / (KT / 32)][i % (KT / 32)] = 0u;
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
@@ -351,11 +369,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     return k0 + KT - 1 > it.p0 || (a.window > 0 && k0 <= plast - a.window);
   };
 
-  // two streams: 384 threads launched with 168 registers each; the row
-  // threads (a row of 128 scores apiece) take 208, the last warpgroup 88
+  // two streams: 384 threads launched with 168 registers each; the row threads
+  // (128 scores apiece) take 216, the last warpgroup 72
   constexpr int kOthers = NS * 128 + 32;  // the row threads and the issuing warp
   if (warp >= kProducer) {
-    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kProducer) {
       if (lane == 0) {
         const uint32_t qb = smem_u32(&bar.q_full);
@@ -382,8 +400,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
             const int phys = PGD_IN(pi, (size_t)a.B * a.max_pages, a.err) ? a.page_table[pi] : -1;
             if (phys < 0 || phys >= a.num_pages) {
               raise_error(a.err, DECODE_ATTN_DEV_BAD_PAGE);
-              atomicMin(&bad_lo_s, ptok);
-              atomicMax(&bad_hi_s, ptok + a.box_t);
+              atomicMin(&sh.bad_lo, ptok);
+              atomicMax(&sh.bad_hi, ptok + a.box_t);
             } else {
               coord = (phys << (a.page_shift - 3)) + ((ptok & (a.page_size - 1)) >> 3);
             }
@@ -394,10 +412,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           int go = 1;
           if (lane == 0) {
             if (!mbar_wait_hot(smem_u32(&bar.empty[slot_r]), ((r / NR) & 1) ^ 1)) {
-              abort_s = 1;
+              sh.abort = 1;
               raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
             }
-            go = abort_s ? 0 : 1;
+            go = *(volatile int32_t*)&sh.abort ? 0 : 1;
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) break;
         }
@@ -419,7 +437,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
 
     if (warp == kMma) {
-      tmem_alloc(smem_u32(&tmem_s), C::kTmemCols);
+      tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
       tc_fence_before();
       named_barrier_sync(1, kOthers);
       tc_fence_after();
@@ -428,25 +446,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       // took 2000 cycles, of which the products need 1100).
       if (elect_one()) {
         if (NS == 2 && ns == 2)
-          chunk_issue<D, E, NS>(bar, smem, tmem_s, ntiles, edge, &abort_s, a);
+          chunk_issue<D, E, NS>(bar, smem, sh.tmem, ntiles, edge, &sh.abort, a);
         else
-          chunk_issue<D, E, 1>(bar, smem, tmem_s, ntiles, edge, &abort_s, a);
+          chunk_issue<D, E, 1>(bar, smem, sh.tmem, ntiles, edge, &sh.abort, a);
       }
       __syncwarp();
       named_barrier_sync(1, kOthers);  // every row has been read out
       tc_fence_after();
-      tmem_free(tmem_s, C::kTmemCols);
+      tmem_free(sh.tmem, C::kTmemCols);
       return;
     }
     // the two warps that look over V's edge tiles
     int edges = 0;
     for (int j = 0; j < ntiles; ++j) {
       if (!edge(j)) continue;
-      if (!mbar_wait_hot(smem_u32(&bar.v_edge), edges & 1)) abort_s = 1;
-      if (!__all_sync(0xffffffffu, !abort_s)) break;
+      if (!mbar_wait_hot(smem_u32(&bar.v_edge), edges & 1)) sh.abort = 1;
+      if (!__all_sync(0xffffffffu, !*(volatile int32_t*)&sh.abort)) break;
       const int k0 = key0 + j * KT;
       uint8_t* vt = ring + ((2 * j + 1) % NR) * C::kTileBytes;
-      if (warp == kMma + 1 && lane == 0 && edges < C::kMaxEdges) edge_key_s[edges] = k0;
+      if (warp == kMma + 1 && lane == 0 && edges < C::kMaxEdges) sh.edge_key[edges] = k0;
       // a quick pass: whether any value of the tile needs a look at all
       const int first = (warp - kMma - 1) * 32 + lane;
       bool look = k0 < it.lo || k0 + KT > it.hi;
@@ -470,8 +488,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         const uint4 m = make_uint4(wild2<E>(v.x), wild2<E>(v.y), wild2<E>(v.z), wild2<E>(v.w));
         if ((m.x | m.y | m.z | m.w) == 0u) continue;
         *at = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
-        if (edges < C::kMaxEdges) atomicOr(&wild_s[edges][t / 32], 1u << (t & 31));
-        wild_any_s = 1;
+        if (edges < C::kMaxEdges) atomicOr(&sh.wild[edges][t / 32], 1u << (t & 31));
+        sh.wild_any = 1;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -482,51 +500,54 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   }
 
   // ---------------------------------------------------------- softmax rows
-  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
   named_barrier_sync(1, kOthers);  // the tensor memory is there
   tc_fence_after();
-  const uint32_t tmem = tmem_s, tmem_o = tmem + 2 * KT;  // O after the two S buffers
+  const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * KT;  // O after the two S buffers
   const int s = warp >> 2;
   if (s < ns) {
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int tok = row / a.G, g = row % a.G;
-    const int ts = it.t0 + s * a.tile_tok;                 // first token of the stream
-    const int te = min(it.t1, ts + a.tile_tok);            // one past its last
-    const bool live = tok < a.tile_tok && ts + tok < te;
-    const int pos = it.p0 + s * a.tile_tok + tok;          // this row's position
+    const int tok = row / a.G;
+    const int te = min(it.t1, it.t0 + (s + 1) * a.tile_tok);  // one past the stream's tokens
     const int first_pos = it.p0 + s * a.tile_tok, last_pos = it.p0 + (te - it.t0) - 1;
-    const bool neg = a.scale_log2 < 0.f;
+    const int pos = first_pos + tok;  // this row's position
+    const float scale = fabsf(a.scale_log2);
     float m = -INFINITY;
     uint64_t l2 = 0;  // two partial sums
     bool ok = true;
-    for (int j = 0; j < ntiles; ++j) {
-      const int u = j * ns + s, buf = u & 1;
-      const uint32_t tm_s = tmem + buf * KT + lanes;
-      if (!mbar_wait_hot(smem_u32(&bar.s_full[buf]), (u >> 1) & 1)) {
-        abort_s = 1;
+    auto wait = [&](uint64_t* b, int parity) {
+      if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
+        sh.abort = 1;
         raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
         ok = false;
       }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+    };
+    for (int j = 0; j < ntiles; ++j) {
+      const int u = j * ns + s, buf = u & 1;
+      const uint32_t tm_s = tmem + buf * KT + lanes;
+      wait(&bar.s_full[buf], (u >> 1) & 1);
+      __syncwarp();
       tc_fence_after();
       float x[KT];
 #pragma unroll
       for (int c = 0; c < KT; c += 32) tmem_ld32(x + c, tm_s + c);
       tmem_wait_ld();
       const int k0 = key0 + j * KT;
-      float mult = fabsf(a.scale_log2);
-      if (neg)
-#pragma unroll
-        for (int i = 0; i < KT; ++i) x[i] = -x[i];
+      float mult = scale;
       if (k0 + KT - 1 > first_pos || (a.window > 0 && k0 <= last_pos - a.window)) {
-        // the edge of some row's range crosses the tile; scaled before the
-        // mask, so that a scale of 0 leaves the mask standing
-        const int top = pos - k0;
-        const int bottom = a.window > 0 ? pos - a.window - k0 : -1;
+        // the edge of some row's range crosses the tile: a bit per key that
+        // the row attends; scaled before the mask, so that a scale of 0
+        // leaves the mask standing
+        const int end = pos - k0 + 1;
+        const int begin = a.window > 0 ? end - a.window : 0;
 #pragma unroll
-        for (int i = 0; i < KT; ++i) x[i] = (i <= top && i > bottom) ? x[i] * mult : -INFINITY;
+        for (int c = 0; c < KT; c += 32) {
+          const uint32_t bits = low_bits(end - c) & ~low_bits(begin - c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[c + i] = (bits & (1u << i)) ? x[c + i] * mult : -INFINITY;
+        }
         mult = 1.f;
       }
       float top[4] = {x[0], x[1], x[2], x[3]};
@@ -539,38 +560,32 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       // The reference maximum follows only when it would grow by more than
       // 2^8: the weights stay below that, and the accumulator is rescaled
       // for a few tiles instead of nearly every one.
-      float alpha = 1.f;
-      if (mx > m + 8.f) {
-        alpha = fast_exp2(m - mx);
-        m = mx;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O holds the products up to the unit before: rescale it in place
-        if (!mbar_wait_hot(smem_u32(&bar.o_full[s]), (j - 1) & 1)) {
-          abort_s = 1;
-          raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
-        }
-        if (!__all_sync(0xffffffffu, !abort_s)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t al = pair(alpha, alpha);
-        l2 = mul2(l2, al);
+      const bool grow = mx > m + 8.f;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = grow ? fast_exp2(m - mx) : 1.f;
+        if (grow) m = mx;
+        if (j > 0) {
+          // O holds the products up to the unit before: rescale it in place
+          wait(&bar.o_full[s], (j - 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+          l2 = mul2(l2, pair(alpha, alpha));
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(o, tmem_o + s * D + lanes + c);
-          tmem_wait_ld();
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            const uint32_t at = tmem_o + s * D + lanes + c;
+            tmem_ld16(o, at);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] *= alpha;
-          tmem_st16(tmem_o + s * D + lanes + c, reinterpret_cast<const uint32_t*>(o));
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
+          }
         }
       }
       const float mu = m == -INFINITY ? 0.f : m;  // a row without a key so far
       const uint64_t mult2 = pair(mult, mult), nm2 = pair(-mu, -mu);
 #pragma unroll
-      for (int part = 0; part < kParts; ++part) {
+      for (int part = 0; part < C::kParts; ++part) {
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -582,38 +597,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         }
         tmem_st32(tm_s + part * 32, w);
         tmem_wait_st();
-        // A parity tells only two neighbouring phases apart: before the last
-        // weights go out, the product before theirs is known to be done (it
-        // is, but for a single stream's), so that the wait after the loop
-        // means the last one.
-        if (part == 0 && j == ntiles - 1 && j > 0 &&
-            !mbar_wait_hot(smem_u32(&bar.o_full[s]), (j - 1) & 1)) {
-          abort_s = 1;
-          raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
-        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar.p_full[buf][part]));
       }
     }
-    if (ok && !mbar_wait_hot(smem_u32(&bar.o_full[s]), (ntiles - 1) & 1)) {
-      abort_s = 1;
-      raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
-    }
-    ok = __all_sync(0xffffffffu, !abort_s);
-    tc_fence_after();
+    wait(&bar.done[s], 0);
     const float2 lh = unpair(l2);
     const float l = lh.x + lh.y;
+    ok = !*(volatile int32_t*)&sh.abort;
+    tc_fence_after();
     // rows that attend a page outside the pool are zeroed
-    const bool dead = !ok || (pos >= bad_lo_s && (a.window <= 0 || pos - a.window + 1 < bad_hi_s));
-    const size_t orow = (size_t)(it.row0 + s * a.tile_tok + tok) * a.Hq + (size_t)h * a.G + g;
-    const bool in = live && PGD_IN(orow, (size_t)a.total * a.Hq, a.err);
+    const bool dead =
+        !ok || (pos >= sh.bad_lo && (a.window <= 0 || pos - a.window + 1 < sh.bad_hi));
+    const size_t orow = (size_t)(it.row0 + s * a.tile_tok + tok) * a.Hq + (size_t)h * a.G +
+                        row % a.G;
+    const bool in = tok < a.tile_tok && it.t0 + s * a.tile_tok + tok < te &&
+                    PGD_IN(orow, (size_t)a.total * a.Hq, a.err);
     // V rows with a NaN or Inf reach the rows that attend them
     auto patch = [&](int c, float (&o)[32]) {
       for (int e = 0; e < C::kMaxEdges; ++e)
         for (int t = 0; t < KT; ++t) {
-          const int key = edge_key_s[e] + t;
-          if (!(wild_s[e][t / 32] >> (t & 31) & 1u) || key > pos ||
+          const int key = sh.edge_key[e] + t;
+          if (!(sh.wild[e][t / 32] >> (t & 31) & 1u) || key > pos ||
               (a.window > 0 && key <= pos - a.window))
             continue;
           const size_t pi = (size_t)it.b * a.max_pages + (key >> a.page_shift);
@@ -631,39 +637,32 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           }
         }
     };
-    if (it.shards == 1) {
-      const float inv = dead || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D);
+    const bool whole = it.shards == 1;
+    const float inv = dead || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+    const size_t slot_w = orow * a.max_shards + shard;
+    if (!whole && in) a.ws_ml[slot_w] = make_float2(m, dead ? -1.f : l);
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        if (ok) tmem_ld32(o, tmem_o + s * D + lanes + c);
-        tmem_wait_ld();
-        if (!in) continue;
-        if (wild_any_s) patch(c, o);
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tmem_ld32(o, tmem_o + s * D + lanes + c);
+      tmem_wait_ld();
+      if (!in) continue;
+      if (sh.wild_any) patch(c, o);
+      if (whole) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          dst[c / 8 + i] = make_uint4(ElemOps<E>::pack2(o[8 * i], o[8 * i + 1]),
-                                      ElemOps<E>::pack2(o[8 * i + 2], o[8 * i + 3]),
-                                      ElemOps<E>::pack2(o[8 * i + 4], o[8 * i + 5]),
-                                      ElemOps<E>::pack2(o[8 * i + 6], o[8 * i + 7]));
-      }
-    } else {
-      const size_t slot_w = orow * a.max_shards + shard;
-      float4* dst = reinterpret_cast<float4*>(a.ws_acc + slot_w * D);
-      if (in) a.ws_ml[slot_w] = make_float2(m, dead ? -1.f : l);
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        if (ok) tmem_ld32(o, tmem_o + s * D + lanes + c);
-        tmem_wait_ld();
-        if (!in || dead) continue;
-        if (wild_any_s) patch(c, o);
+          dst[i] = make_uint4(ElemOps<E>::pack2(o[8 * i], o[8 * i + 1]),
+                              ElemOps<E>::pack2(o[8 * i + 2], o[8 * i + 3]),
+                              ElemOps<E>::pack2(o[8 * i + 4], o[8 * i + 5]),
+                              ElemOps<E>::pack2(o[8 * i + 6], o[8 * i + 7]));
+      } else if (!dead) {
+        float4* dst = reinterpret_cast<float4*>(a.ws_acc + slot_w * D + c);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dst[c / 4 + i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
     }
     tc_fence_before();

@@ -98,6 +98,8 @@ __host__ __device__ constexpr uint32_t tc_idesc(int m, int n, bool bf16, bool b_
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+constexpr uint32_t kIdescNegA = 1u << 13;  // negate A
+
 // Shared-memory operand descriptor with the 128-byte swizzle; lbo and sbo in
 // bytes.  K-major: sbo is the distance between groups of 8 rows.  MN-major:
 // lbo is the distance between chunks of 64 columns, sbo the distance between
