@@ -488,50 +488,130 @@ def decode_attn_static_scratch(q, k_pages, v_pages, page_table, seq_lens, scale:
 
 
 # ------------------------------------------------ new tokens by the chunk
+#
+# A small call is bound by what the host does before its launch, so these
+# functions look at each tensor once (`_is`) and leave the wording of an error
+# to the slower checks.
 
-def _scratch(device, nbytes: int, zero: bool, stream=None):
-    """A workspace for one call of the entry points below: cached per
-    (device, stream) like decode_attn's, but a call under stream capture gets
-    one of its own, so that two captured graphs never share one."""
+def _is(t, dtype, index) -> bool:
+    """A contiguous tensor of this type on CUDA device `index`."""
+    return t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+
+
+def _need(t, dtype, name, index):
+    import torch
+    if not (isinstance(t, torch.Tensor) and _is(t, dtype, index)):
+        _check(t, dtype, name, torch.device("cuda", index) if index >= 0 else None)
+
+
+def _cuda_index(t, name: str, call: str) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{call} runs on CUDA tensors")
+    return t.get_device()
+
+
+def _raw_stream(stream, index: int) -> int:
+    """_stream_handle for tensors on the current device `index`."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream_handle(stream)
+
+
+def _scratch(index: int, nbytes: int, zero: bool, stream):
+    """A workspace for one call: cached per (device, stream) like
+    decode_attn's, but a call under stream capture gets one of its own, so
+    that two captured graphs never share one."""
     import torch
     if nbytes == 0:
         return None
-    index = device.index if device.index is not None else torch.cuda.current_device()
-    s = stream if stream is not None else torch.cuda.current_stream(index)
-    with torch.cuda.stream(s):
-        capturing = torch.cuda.is_current_stream_capturing()
-        key = (index, s.cuda_stream, zero)
-        buf = None if capturing else _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            make = torch.zeros if zero else torch.empty
-            buf = make(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-            if not capturing:
-                _ws_cache[key] = buf
+    if stream is not None and stream != torch.cuda.current_stream(index):
+        with torch.cuda.stream(stream):
+            return _scratch(index, nbytes, zero, None)
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = (index, _raw_stream(None, index), zero)
+    buf = None if capturing else _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        make = torch.zeros if zero else torch.empty
+        buf = make(max(nbytes, 1 << 20), dtype=torch.uint8, device=torch.device("cuda", index))
+        if not capturing:
+            _ws_cache[key] = buf
     return buf
 
 
-def _check_offsets(t, batch: int, name: str, device):
+def _check_offsets(t, batch: int, name: str, index: int):
     import torch
-    _check(t, torch.int32, name, device)
-    if tuple(t.shape) != (batch + 1,):
+    _need(t, torch.int32, name, index)
+    if t.shape != (batch + 1,):
         raise ValueError(f"{name} must be [B + 1] = [{batch + 1}], got {list(t.shape)}")
 
 
-def _check_table(page_table, seq_lens, device):
+def _check_table(page_table, seq_lens, index: int) -> int:
+    """The batch, after checking the table (and the lengths, if any)."""
     import torch
-    _check(page_table, torch.int32, "page_table", device)
+    _need(page_table, torch.int32, "page_table", index)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
+    batch = page_table.shape[0]
     if seq_lens is not None:
-        _check(seq_lens, torch.int32, "seq_lens", device)
-        if tuple(seq_lens.shape) != (page_table.shape[0],):
-            raise ValueError(f"seq_lens must be [B] = [{page_table.shape[0]}]")
+        _need(seq_lens, torch.int32, "seq_lens", index)
+        if seq_lens.shape != (batch,):
+            raise ValueError(f"seq_lens must be [B] = [{batch}]")
+    return batch
 
 
-def _check_err_flag(err_flag, device):
+def _err_ptr(err_flag, index: int) -> Optional[int]:
     import torch
-    if err_flag is not None:
-        _check(err_flag, torch.int32, "err_flag", device)
+    if err_flag is None:
+        return None
+    _need(err_flag, torch.int32, "err_flag", index)
+    return err_flag.data_ptr()
+
+
+def _ws_args(workspace, index: int):
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _kv_pools(k_pages, v_pages, k_scales, v_scales, index: int) -> int:
+    """The cell format of a pair of pools, after checking them (and the
+    scales an 8-bit pair needs)."""
+    import torch
+    if not isinstance(k_pages, torch.Tensor):
+        raise TypeError("k_pages must be a torch.Tensor")
+    quant = k_pages.dtype is torch.float8_e4m3fn
+    dt = k_pages.dtype if quant else _elem_dtype(k_pages)
+    _need(k_pages, dt, "k_pages", index)
+    _need(v_pages, dt, "v_pages", index)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [P, PS, Hkv, D], both of one shape")
+    if not quant:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("k_scales and v_scales go with float8_e4m3fn pools only")
+        return KV_16BIT
+    P, PS, Hkv, _ = k_pages.shape
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t is None:
+            raise ValueError(f"float8_e4m3fn pools need {name}")
+        _need(t, torch.float32, name, index)
+        if t.shape != (P, Hkv, PS):
+            raise ValueError(f"{name} must be [P, Hkv, PS] = [{P}, {Hkv}, {PS}]")
+    return KV_E4M3
+
+
+def _params(B, Hq, pool_shape, max_pages, max_seq_len, scale, window, dtype, split_min=0,
+            force_chunk=0, T=1, schedule=0) -> DecodeAttnParams:
+    import torch
+    P, PS, Hkv, D = pool_shape
+    return DecodeAttnParams(B, Hq, Hkv, D, PS, max_pages, P, max_seq_len or 0, scale, window, 0,
+                            split_min, force_chunk, T,
+                            DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP16, schedule)
 
 
 def decode_attn_chunk_make_plan(params: DecodeAttnParams, total_queries: int,
@@ -550,7 +630,6 @@ def decode_attn_chunk_workspace_size(params: DecodeAttnParams, total_queries: in
         ctypes.byref(params), int(total_queries), int(device)))
 
 
-@_on_device_of("q", 0)
 def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, scale: float,
                       window: int = 0, out=None, max_seq_len: Optional[int] = None,
                       workspace=None, err_flag=None, force_chunk: int = 0, stream=None):
@@ -564,76 +643,48 @@ def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, 
     sequence owns keep what they held (a new ``out`` is not initialised).
     ``max_seq_len`` (a host-side bound) only steers the plan."""
     import torch
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("decode_attn_chunk runs on CUDA tensors")
+    index = _cuda_index(q, "q", "decode_attn_chunk")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens,
+                                     scale, window, out, max_seq_len, workspace, err_flag,
+                                     force_chunk, stream)
     et = _elem_dtype(q)
-    _check(q, et, "q", dev)
+    _need(q, et, "q", index)
     if q.dim() != 3:
         raise ValueError("q must be [total, Hq, D]")
-    _check(k_pages, et, "k_pages", dev)
-    _check(v_pages, et, "v_pages", dev)
+    _need(k_pages, et, "k_pages", index)
+    _need(v_pages, et, "v_pages", index)
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must be [P, PS, Hkv, D], both of one shape")
-    _check_table(page_table, seq_lens, dev)
-    _check_offsets(query_offsets, page_table.shape[0], "query_offsets", dev)
-    _check_err_flag(err_flag, dev)
-    total, B = q.shape[0], page_table.shape[0]
-    p = make_params(q, k_pages, page_table, scale, window, max_seq_len, 0, 0, force_chunk)
-    p.batch, p.num_queries = B, 1
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch.Tensor")
+    B = _check_table(page_table, seq_lens, index)
+    _check_offsets(query_offsets, B, "query_offsets", index)
+    total, Hq, D = q.shape
+    if k_pages.shape[3] != D:
+        raise ValueError("q and k_pages head_dim differ")
     if out is None:
         out = torch.empty_like(q)
-    _check(out, et, "out", dev)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+    else:
+        _need(out, et, "out", index)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    p = _params(B, Hq, k_pages.shape, page_table.shape[1], max_seq_len, scale, window, et, 0,
+                force_chunk)
+    lib, ref = load_library(), ctypes.byref(p)
     if workspace is None:
-        workspace = _scratch(dev, decode_attn_chunk_workspace_size(
-            p, total, dev.index if dev.index is not None else torch.cuda.current_device()),
-            False, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load_library().decode_attn_chunk(
-        ctypes.byref(p), total, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-        _ptr(query_offsets), _ptr(seq_lens), _ptr(out), _ptr(workspace), ws_bytes,
-        _ptr(err_flag), _stream_handle(stream))
+        workspace = _scratch(index, lib.decode_attn_chunk_workspace_size(ref, total, index),
+                             False, stream)
+    st = lib.decode_attn_chunk(ref, total, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                               page_table.data_ptr(), query_offsets.data_ptr(),
+                               seq_lens.data_ptr(), out.data_ptr(), *_ws_args(workspace, index),
+                               _err_ptr(err_flag, index), _raw_stream(stream, index))
     if st:
         raise DecodeAttnError(st, "decode_attn_chunk")
     return out
 
 
-def _kv_pools(k_pages, v_pages, k_scales, v_scales, device):
-    """The cell format of a pair of pools, after checking them (and the
-    scales an 8-bit pair needs)."""
-    import torch
-    if not isinstance(k_pages, torch.Tensor):
-        raise TypeError("k_pages must be a torch.Tensor")
-    quant = k_pages.dtype == torch.float8_e4m3fn
-    dt = k_pages.dtype if quant else _elem_dtype(k_pages)
-    _check(k_pages, dt, "k_pages", device)
-    _check(v_pages, dt, "v_pages", device)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must be [P, PS, Hkv, D], both of one shape")
-    P, PS, Hkv, _ = k_pages.shape
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if not quant:
-            if t is not None:
-                raise ValueError(f"{name} goes with float8_e4m3fn pools only")
-            continue
-        if t is None:
-            raise ValueError(f"float8_e4m3fn pools need {name}")
-        _check(t, torch.float32, name, device)
-        if tuple(t.shape) != (P, Hkv, PS):
-            raise ValueError(f"{name} must be [P, Hkv, PS] = [{P}, {Hkv}, {PS}]")
-    return KV_E4M3 if quant else KV_16BIT
-
-
-def _rows_params(k_pages, page_table, dtype_code: int) -> DecodeAttnParams:
-    P, PS, Hkv, D = k_pages.shape
-    return DecodeAttnParams(batch=page_table.shape[0], num_q_heads=Hkv, num_kv_heads=Hkv,
-                            head_dim=D, page_size=PS, max_pages_per_seq=page_table.shape[1],
-                            num_pages=P, scale=1.0, num_queries=1, dtype=dtype_code)
-
-
-@_on_device_of("k_pages", 4)
 def decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages, page_table,
                            k_scales=None, v_scales=None, err_flag=None, stream=None):
     """Writes a ragged batch's new rows k_new/v_new [total, Hkv, D] (fp16 or
@@ -643,31 +694,31 @@ def decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages
     codes, and k_scales/v_scales [P, Hkv, PS] float32 a power of two per row
     and head."""
     import torch
-    dev = k_pages.device
-    if dev.type != "cuda":
-        raise ValueError("decode_kv_append_chunk runs on CUDA tensors")
-    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
+    index = _cuda_index(k_pages, "k_pages", "decode_kv_append_chunk")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages,
+                                          page_table, k_scales, v_scales, err_flag, stream)
+    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, index)
     et = _elem_dtype(k_new) if fmt == KV_E4M3 else k_pages.dtype
-    _check(k_new, et, "k_new", dev)
-    _check(v_new, et, "v_new", dev)
-    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != tuple(k_pages.shape[2:]) or \
-            v_new.shape != k_new.shape:
+    _need(k_new, et, "k_new", index)
+    _need(v_new, et, "v_new", index)
+    if k_new.dim() != 3 or k_new.shape[1:] != k_pages.shape[2:] or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be [total, Hkv, D]")
     if seq_lens is None:
         raise TypeError("seq_lens must be a torch.Tensor")
-    _check_table(page_table, seq_lens, dev)
-    _check_offsets(row_offsets, page_table.shape[0], "row_offsets", dev)
-    _check_err_flag(err_flag, dev)
-    p = _rows_params(k_pages, page_table, _dtype_code(k_new))
+    B = _check_table(page_table, seq_lens, index)
+    _check_offsets(row_offsets, B, "row_offsets", index)
+    p = _params(B, k_pages.shape[2], k_pages.shape, page_table.shape[1], 0, 1.0, 0, et)
     st = load_library().decode_kv_append_chunk(
-        ctypes.byref(p), fmt, k_new.shape[0], _ptr(k_new), _ptr(v_new), _ptr(row_offsets),
-        _ptr(seq_lens), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-        _ptr(page_table), _ptr(err_flag), _stream_handle(stream))
+        ctypes.byref(p), fmt, k_new.shape[0], k_new.data_ptr(), v_new.data_ptr(),
+        row_offsets.data_ptr(), seq_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(), _err_ptr(err_flag, index),
+        _raw_stream(stream, index))
     if st:
         raise DecodeAttnError(st, "decode_kv_append_chunk")
 
 
-@_on_device_of("k_pages", 0)
 def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, starts=None,
                    k_scales=None, v_scales=None, dtype=None, k_out=None, v_out=None,
                    err_flag=None, stream=None):
@@ -678,18 +729,18 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
     or k_out / v_out as given; rows that no sequence owns keep what they held
     (new outputs are not initialised)."""
     import torch
-    dev = k_pages.device
-    if dev.type != "cuda":
-        raise ValueError("decode_kv_read runs on CUDA tensors")
-    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
-    _check_table(page_table, None, dev)
-    B = page_table.shape[0]
-    _check_offsets(row_offsets, B, "row_offsets", dev)
+    index = _cuda_index(k_pages, "k_pages", "decode_kv_read")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows, starts,
+                                  k_scales, v_scales, dtype, k_out, v_out, err_flag, stream)
+    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, index)
+    B = _check_table(page_table, None, index)
+    _check_offsets(row_offsets, B, "row_offsets", index)
     if starts is not None:
-        _check(starts, torch.int32, "starts", dev)
-        if tuple(starts.shape) != (B,):
+        _need(starts, torch.int32, "starts", index)
+        if starts.shape != (B,):
             raise ValueError(f"starts must be [B] = [{B}]")
-    _check_err_flag(err_flag, dev)
     if dtype is None:
         given = k_out if k_out is not None else v_out
         dtype = k_pages.dtype if fmt == KV_16BIT else \
@@ -699,22 +750,24 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
     if fmt == KV_16BIT and dtype != k_pages.dtype:
         raise TypeError(f"16-bit pools are read back as they are ({k_pages.dtype})")
     shape = (int(total_rows), *k_pages.shape[2:])
-    outs = []
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        _check(t, dtype, name, dev)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
-        outs.append(t)
-    p = _rows_params(k_pages, page_table, _dtype_code(outs[0]))
+    if k_out is None and v_out is None:  # one allocation
+        k_out, v_out = torch.empty((2, *shape), dtype=dtype, device=k_pages.device).unbind(0)
+    else:
+        k_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if v_out is None else v_out
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            _need(t, dtype, name, index)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
+    p = _params(B, k_pages.shape[2], k_pages.shape, page_table.shape[1], 0, 1.0, 0, dtype)
     st = load_library().decode_kv_read(
-        ctypes.byref(p), fmt, shape[0], _ptr(k_pages), _ptr(v_pages), _ptr(k_scales),
-        _ptr(v_scales), _ptr(page_table), _ptr(row_offsets), _ptr(starts), _ptr(outs[0]),
-        _ptr(outs[1]), _ptr(err_flag), _stream_handle(stream))
+        ctypes.byref(p), fmt, shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+        _ptr(v_scales), page_table.data_ptr(), row_offsets.data_ptr(), _ptr(starts),
+        k_out.data_ptr(), v_out.data_ptr(), _err_ptr(err_flag, index),
+        _raw_stream(stream, index))
     if st:
         raise DecodeAttnError(st, "decode_kv_read")
-    return outs[0], outs[1]
+    return k_out, v_out
 
 
 def decode_attn_quant_make_plan(params: DecodeAttnParams, num_sms: int,
@@ -733,7 +786,6 @@ def decode_attn_quant_workspace_size(params: DecodeAttnParams, device: int,
         ctypes.byref(params), int(kv_format), int(device)))
 
 
-@_on_device_of("q", 0)
 def decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens,
                       scale: float, window: int = 0, out=None,
                       max_seq_len: Optional[int] = None, workspace=None, err_flag=None,
@@ -744,35 +796,45 @@ def decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_l
     scale).  q [B, Hq, D] (or [B, T, Hq, D]) fp16 or bf16; returns ``out``
     like q."""
     import torch
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("decode_attn_quant runs on CUDA tensors")
+    index = _cuda_index(q, "q", "decode_attn_quant")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table,
+                                     seq_lens, scale, window, out, max_seq_len, workspace,
+                                     err_flag, split_min, force_chunk, stream, schedule)
     et = _elem_dtype(q)
-    _check(q, et, "q", dev)
-    if q.dim() not in (3, 4):
+    _need(q, et, "q", index)
+    if q.dim() == 3:
+        (B, Hq, D), T = q.shape, 1
+    elif q.dim() == 4:
+        B, T, Hq, D = q.shape
+    else:
         raise ValueError("q must be [B, Hq, D] or [B, T, Hq, D]")
-    fmt = _kv_pools(k_pages, v_pages, k_scales, v_scales, dev)
-    if fmt != KV_E4M3:
+    if _kv_pools(k_pages, v_pages, k_scales, v_scales, index) != KV_E4M3:
         raise TypeError(f"decode_attn_quant takes float8_e4m3fn pools, got {k_pages.dtype}")
-    _check_table(page_table, seq_lens, dev)
-    if page_table.shape[0] != q.shape[0]:
+    if k_pages.shape[3] != D:
+        raise ValueError("q and k_pages head_dim differ")
+    if seq_lens is None:
+        raise TypeError("seq_lens must be a torch.Tensor")
+    if _check_table(page_table, seq_lens, index) != B:
         raise ValueError("page_table must have a row for each sequence of q")
-    _check_err_flag(err_flag, dev)
-    p = make_params(q, k_pages, page_table, scale, window, max_seq_len, VARIANT_AUTO, split_min,
-                    force_chunk, schedule)
     if out is None:
         out = torch.empty_like(q)
-    _check(out, et, "out", dev)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+    else:
+        _need(out, et, "out", index)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    p = _params(B, Hq, k_pages.shape, page_table.shape[1], max_seq_len, scale, window, et,
+                split_min, force_chunk, T, schedule)
+    lib, ref = load_library(), ctypes.byref(p)
     if workspace is None:
-        workspace = _scratch(dev, decode_attn_quant_workspace_size(
-            p, dev.index if dev.index is not None else torch.cuda.current_device()), True, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load_library().decode_attn_quant(
-        ctypes.byref(p), fmt, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales),
-        _ptr(v_scales), _ptr(page_table), _ptr(seq_lens), _ptr(out), _ptr(workspace), ws_bytes,
-        _ptr(err_flag), _stream_handle(stream))
+        workspace = _scratch(index, lib.decode_attn_quant_workspace_size(ref, KV_E4M3, index),
+                             True, stream)
+    st = lib.decode_attn_quant(ref, KV_E4M3, q.data_ptr(), k_pages.data_ptr(),
+                               v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                               page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                               *_ws_args(workspace, index), _err_ptr(err_flag, index),
+                               _raw_stream(stream, index))
     if st:
         raise DecodeAttnError(st, "decode_attn_quant")
     return out

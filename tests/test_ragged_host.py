@@ -193,7 +193,7 @@ def test_binding_refuses_host_tensors(pkg):
 
 
 def test_binding_checks_pools_and_scales(pkg):
-    x, dev = tensors(), torch.device("cpu")
+    x, dev = tensors(), -1  # the index of a CPU tensor
     assert pkg._kv_pools(x["k"], x["k"], None, None, dev) == pkg.KV_16BIT
     assert pkg._kv_pools(x["codes"], x["codes"], x["s"], x["s"], dev) == pkg.KV_E4M3
     for bad, exc in (((x["k"], x["k"], x["s"], None), ValueError),
@@ -212,7 +212,7 @@ def test_binding_checks_pools_and_scales(pkg):
 
 
 def test_binding_checks_offsets_and_tables(pkg):
-    x, dev = tensors(), torch.device("cpu")
+    x, dev = tensors(), -1  # the index of a CPU tensor
     pkg._check_offsets(x["off"], 2, "off", dev)
     for bad, exc in ((x["off"][:2], ValueError), (x["off"].long(), TypeError),
                      (x["off"].view(3, 1), ValueError), ([0, 1, 2], TypeError)):
