@@ -23,6 +23,11 @@ import os
 import threading
 from typing import Optional
 
+try:
+    import torch
+except ImportError:  # the C ABI and the planners need no torch
+    torch = None
+
 __all__ = [
     "DecodeAttnParams", "DecodeAttnPlan", "DecodeAttnError", "load_library", "library_path",
     "make_params", "decode_attn", "decode_attn_split", "decode_attn_combine",
@@ -490,22 +495,17 @@ def decode_attn_static_scratch(q, k_pages, v_pages, page_table, seq_lens, scale:
 # ------------------------------------------------ new tokens by the chunk
 #
 # A small call is bound by what the host does before its launch, so these
-# functions look at each tensor once (`_is`) and leave the wording of an error
-# to the slower checks.
-
-def _is(t, dtype, index) -> bool:
-    """A contiguous tensor of this type on CUDA device `index`."""
-    return t.dtype is dtype and t.get_device() == index and t.is_contiguous()
-
+# functions look at each tensor once and leave the wording of an error to the
+# slower checks.
 
 def _need(t, dtype, name, index):
-    import torch
-    if not (isinstance(t, torch.Tensor) and _is(t, dtype, index)):
+    """A contiguous tensor of this type on CUDA device `index`."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and
+            t.is_contiguous()):
         _check(t, dtype, name, torch.device("cuda", index) if index >= 0 else None)
 
 
 def _cuda_index(t, name: str, call: str) -> int:
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -516,8 +516,7 @@ def _cuda_index(t, name: str, call: str) -> int:
 def _raw_stream(stream, index: int) -> int:
     """_stream_handle for tensors on the current device `index`."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
+            return torch._C._cuda_getCurrentRawStream(index)
     return _stream_handle(stream)
 
 
@@ -525,7 +524,6 @@ def _scratch(index: int, nbytes: int, zero: bool, stream):
     """A workspace for one call: cached per (device, stream) like
     decode_attn's, but a call under stream capture gets one of its own, so
     that two captured graphs never share one."""
-    import torch
     if nbytes == 0:
         return None
     if stream is not None and stream != torch.cuda.current_stream(index):
@@ -543,7 +541,6 @@ def _scratch(index: int, nbytes: int, zero: bool, stream):
 
 
 def _check_offsets(t, batch: int, name: str, index: int):
-    import torch
     _need(t, torch.int32, name, index)
     if t.shape != (batch + 1,):
         raise ValueError(f"{name} must be [B + 1] = [{batch + 1}], got {list(t.shape)}")
@@ -551,7 +548,6 @@ def _check_offsets(t, batch: int, name: str, index: int):
 
 def _check_table(page_table, seq_lens, index: int) -> int:
     """The batch, after checking the table (and the lengths, if any)."""
-    import torch
     _need(page_table, torch.int32, "page_table", index)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
@@ -564,7 +560,6 @@ def _check_table(page_table, seq_lens, index: int) -> int:
 
 
 def _err_ptr(err_flag, index: int) -> Optional[int]:
-    import torch
     if err_flag is None:
         return None
     _need(err_flag, torch.int32, "err_flag", index)
@@ -582,7 +577,6 @@ def _ws_args(workspace, index: int):
 def _kv_pools(k_pages, v_pages, k_scales, v_scales, index: int) -> int:
     """The cell format of a pair of pools, after checking them (and the
     scales an 8-bit pair needs)."""
-    import torch
     if not isinstance(k_pages, torch.Tensor):
         raise TypeError("k_pages must be a torch.Tensor")
     quant = k_pages.dtype is torch.float8_e4m3fn
@@ -607,7 +601,6 @@ def _kv_pools(k_pages, v_pages, k_scales, v_scales, index: int) -> int:
 
 def _params(B, Hq, pool_shape, max_pages, max_seq_len, scale, window, dtype, split_min=0,
             force_chunk=0, T=1, schedule=0) -> DecodeAttnParams:
-    import torch
     P, PS, Hkv, D = pool_shape
     return DecodeAttnParams(B, Hq, Hkv, D, PS, max_pages, P, max_seq_len or 0, scale, window, 0,
                             split_min, force_chunk, T,
@@ -642,7 +635,6 @@ def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, 
     ``window`` of them with a window.  Returns ``out`` like q; rows that no
     sequence owns keep what they held (a new ``out`` is not initialised).
     ``max_seq_len`` (a host-side bound) only steers the plan."""
-    import torch
     index = _cuda_index(q, "q", "decode_attn_chunk")
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
@@ -693,7 +685,6 @@ def decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages
     them).  16-bit pools get the rows bit for bit; float8_e4m3fn pools get
     codes, and k_scales/v_scales [P, Hkv, PS] float32 a power of two per row
     and head."""
-    import torch
     index = _cuda_index(k_pages, "k_pages", "decode_kv_append_chunk")
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
@@ -728,7 +719,6 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
     pools' own for 16-bit pools; by default float16 for float8_e4m3fn ones)
     or k_out / v_out as given; rows that no sequence owns keep what they held
     (new outputs are not initialised)."""
-    import torch
     index = _cuda_index(k_pages, "k_pages", "decode_kv_read")
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
@@ -750,15 +740,14 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
     if fmt == KV_16BIT and dtype != k_pages.dtype:
         raise TypeError(f"16-bit pools are read back as they are ({k_pages.dtype})")
     shape = (int(total_rows), *k_pages.shape[2:])
-    if k_out is None and v_out is None:  # one allocation
-        k_out, v_out = torch.empty((2, *shape), dtype=dtype, device=k_pages.device).unbind(0)
-    else:
-        k_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=k_pages.device) if v_out is None else v_out
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            _need(t, dtype, name, index)
-            if t.shape != shape:
-                raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _need(t, dtype, name, index)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
     p = _params(B, k_pages.shape[2], k_pages.shape, page_table.shape[1], 0, 1.0, 0, dtype)
     st = load_library().decode_kv_read(
         ctypes.byref(p), fmt, shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
@@ -795,7 +784,6 @@ def decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_l
     float8_e4m3fn with k_scales/v_scales [P, Hkv, PS] float32 (value = code *
     scale).  q [B, Hq, D] (or [B, T, Hq, D]) fp16 or bf16; returns ``out``
     like q."""
-    import torch
     index = _cuda_index(q, "q", "decode_attn_quant")
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):

@@ -13,9 +13,9 @@ namespace {
 constexpr size_t kTicketRegion = 64 * 1024;
 constexpr int kDefaultSplitMin = 256;
 constexpr int kMinChunk = 128;
-constexpr int kCtasPerSm = 2;  // 96 KiB of ring each
-constexpr int kLargeChunkCap = 4096;
-constexpr double kRingBytes = 96 * 1024;
+constexpr int kLargeChunkCap = 2048;
+constexpr int64_t kPairBytes = 64 << 20;
+constexpr double kSmRingBytes = 192 * 1024;  // in flight per SM
 // The one-wave cost model of the 16-bit planner: the read rate, the loaded
 // round trip in which a CTA moves its ring, the merge per 8 shards, and the
 // share of the CTA slots a one-wave grid fills.
@@ -29,9 +29,22 @@ size_t ticket_bytes(const decode_attn_params* p) {
                   (size_t)round_up(((int64_t)p->batch * p->num_kv_heads + 64) * 4, 256));
 }
 
+// KV heads of a CTA: two where the box of a page's piece of one head is at most
+// 4 KB and the step is large (QuantArgs).  With boxes of 8 KB it depends on the
+// plan (four sequences of 131072 positions 191 -> 185 us, one of them 58 -> 72,
+// eight of 16384 52 -> 113: half the units, so twice the shards to merge), and
+// a small step has too few CTAs as it is.
+int heads_per_cta(const decode_attn_params* p, int64_t span) {
+  const int rows = queries(p) * (p->num_q_heads / p->num_kv_heads);
+  const int64_t box = (int64_t)std::min(p->page_size, kTile) * p->head_dim;
+  const int64_t bytes = (int64_t)p->batch * p->num_kv_heads * span * 2 * p->head_dim;
+  return rows <= 8 && p->num_kv_heads % 2 == 0 && box <= 4096 && bytes >= kPairBytes ? 2 : 1;
+}
+
 // Shards of a sequence when the grid is one wave: least t(S) = bytes /
 // min(read rate, CTAs * ring / round trip) + the merge, ties to more CTAs.
-int64_t one_wave(int64_t units, int64_t slots, int64_t span, double row_bytes, int64_t max_chunk) {
+int64_t one_wave(int64_t units, int64_t slots, int64_t span, double row_bytes, int64_t max_chunk,
+                 double ring_bytes) {
   const double bytes = (double)units * (double)span * row_bytes;
   const int64_t s_lo = std::max<int64_t>(2, ceil_div(span, max_chunk));
   const int64_t fill = std::max<int64_t>(1, (int64_t)(kOneWaveFill * (double)slots) / units);
@@ -42,7 +55,8 @@ int64_t one_wave(int64_t units, int64_t slots, int64_t span, double row_bytes, i
     const int64_t chunk = round_up(ceil_div(span, s), kTile);
     if (chunk > max_chunk) continue;
     const int64_t got = ceil_div(span, chunk);
-    const double rate = std::min(kStreamBytesPerS, (double)(units * got) * kRingBytes / kRoundTripS);
+    const double rate =
+        std::min(kStreamBytesPerS, (double)(units * got) * ring_bytes / kRoundTripS);
     const double t = bytes / rate + (got > 1 ? kMergeStepS * (double)ceil_div(got, 8) : 0.0);
     if (t < best_t * (1 - 1e-3) || (t <= best_t * (1 + 1e-3) && got > best)) {
       best = got;
@@ -72,10 +86,13 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
   const int64_t attended =
       p->window > 0 ? std::min<int64_t>(max_len, (int64_t)p->window + T - 1) : max_len;
   const int64_t span = std::max<int64_t>(1, p->window > 0 ? attended + kTile - 1 : max_len);
-  const int64_t max_chunk = (int64_t)kMaxPieces * std::min(p->page_size, kTile);
-  const int64_t units = std::max<int64_t>(1, (int64_t)p->batch * p->num_kv_heads);
-  const int64_t slots = (int64_t)num_sms * kCtasPerSm;
-  const double row_bytes = 2.0 * D + 8;  // a position's K and V codes and scales of one head
+  const int HC = heads_per_cta(p, span);
+  const int kv_heads = p->num_kv_heads / HC;
+  const int64_t max_chunk = (int64_t)kMaxPieces * std::min(p->page_size, kTile / HC);
+  const int64_t units = std::max<int64_t>(1, (int64_t)p->batch * kv_heads);
+  const int ctas_per_sm = D == 256 ? QuantCfg<256>::kCtas : QuantCfg<128>::kCtas;
+  const int64_t slots = (int64_t)num_sms * ctas_per_sm;
+  const double row_bytes = HC * (2.0 * D + 8);  // a position's K and V codes and scales
   const int split_min = p->split_min > 0 ? p->split_min : kDefaultSplitMin;
 
   int64_t chunk;
@@ -86,8 +103,8 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
     chunk = std::min(round_up(span, kTile), max_chunk);
   } else {
     int64_t s;
-    if (units < slots) {
-      s = one_wave(units, slots, span, row_bytes, max_chunk);
+    if (2 * units <= (int64_t)(kOneWaveFill * (double)slots)) {
+      s = one_wave(units, slots, span, row_bytes, max_chunk, kSmRingBytes / ctas_per_sm);
     } else if ((double)units * span * row_bytes <= (double)slots * (1 << 20)) {
       s = std::max<int64_t>(1, std::min(slots / units, ceil_div(span, kMinChunk)));
     } else {
@@ -100,7 +117,7 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
   }
   const int64_t shards = ceil_div(span, chunk);
   if (shards > 65535) return DECODE_ATTN_ERR_SHAPE;
-  const int64_t ctas = (int64_t)p->batch * p->num_kv_heads * shards;
+  const int64_t ctas = (int64_t)p->batch * kv_heads * shards;
   const bool one_wave_grid = ctas <= slots;
 
   plan->variant = DECODE_ATTN_VARIANT_MMA;
@@ -111,10 +128,10 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
   plan->split = shards > 1 ? 1 : 0;
   plan->head_fastest = one_wave_grid ? 0 : 1;
   plan->balanced = plan->split && one_wave_grid && p->force_chunk <= 0 ? 1 : 0;
-  plan->grid_x = plan->head_fastest ? p->num_kv_heads : (int32_t)shards;
-  plan->grid_y = plan->head_fastest ? (int32_t)shards : p->num_kv_heads;
+  plan->grid_x = plan->head_fastest ? kv_heads : (int32_t)shards;
+  plan->grid_y = plan->head_fastest ? (int32_t)shards : kv_heads;
   plan->grid_z = p->batch;
-  plan->ctas_per_sm = kCtasPerSm;
+  plan->ctas_per_sm = ctas_per_sm;
   plan->ring_stages = D == 64 ? QuantCfg<64>::kStages
                               : D == 128 ? QuantCfg<128>::kStages : QuantCfg<256>::kStages;
   // the merge, by the 16-bit planner's rule: a cluster for one-wave plans of
@@ -166,7 +183,10 @@ extern "C" int decode_attn_quant(const decode_attn_params* p, int32_t kv_format,
     return DECODE_ATTN_ERR_WORKSPACE;
   if (p->batch == 0) return DECODE_ATTN_OK;
 
-  const int D = p->head_dim, box_t = std::min(p->page_size, kTile);
+  const int D = p->head_dim;
+  const int kv_heads = plan.head_fastest ? plan.grid_x : plan.grid_y;
+  const int HC = p->num_kv_heads / kv_heads;
+  const int box_t = std::min(p->page_size, kTile / HC);
   QuantLaunch L{};
   for (int i = 0; i < 2; ++i) {
     // [P][PS][Hkv][D] codes as (up to 128 dims, row, head, chunk of 128
@@ -175,7 +195,7 @@ extern "C" int decode_attn_quant(const decode_attn_params* p, int32_t kv_format,
     const uint64_t dims[4] = {w, (uint64_t)p->num_pages * p->page_size,
                               (uint64_t)p->num_kv_heads, (uint64_t)D / w};
     const uint64_t strides[3] = {row, (uint64_t)D, w};
-    const uint32_t box[4] = {(uint32_t)w, (uint32_t)box_t, 1, (uint32_t)(D / w)};
+    const uint32_t box[4] = {(uint32_t)w, (uint32_t)box_t, (uint32_t)HC, (uint32_t)(D / w)};
     st = encode_map(i ? &L.tmap_v : &L.tmap_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                     i ? v_pages : k_pages, dims, strides, box);
     if (st) return st;
@@ -197,8 +217,10 @@ extern "C" int decode_attn_quant(const decode_attn_params* p, int32_t kv_format,
     a.ws_acc = reinterpret_cast<float*>(base + tickets + round_up(rows * sizeof(float2), 256));
   }
   a.Hq = p->num_q_heads;
-  a.Hkv = p->num_kv_heads;
-  a.G = p->num_q_heads / p->num_kv_heads;
+  a.Hkv = kv_heads;
+  a.G = p->num_q_heads / kv_heads;
+  L.args.G1 = p->num_q_heads / p->num_kv_heads;
+  L.args.heads = p->num_kv_heads;
   a.max_pages = p->max_pages_per_seq;
   a.num_pages = p->num_pages;
   a.page_size = p->page_size;

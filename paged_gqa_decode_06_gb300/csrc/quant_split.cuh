@@ -29,41 +29,55 @@
 
 #include "e4m3.cuh"
 #include "split_mma.cuh"
+#include "tcgen05.cuh"  // mbar_wait_hot
 
 namespace pgd {
 
+// A CTA takes HC = 1 or 2 neighbouring KV heads.  Two, where one head's box of
+// a page's piece is too small for the copy engine: a box costs about 45 ns
+// whatever it brings, and a box can hold the rows of several heads (GB300,
+// pages of 16: 64 sequences of U[1, 8192] positions 125 -> 114 us, a thousand
+// of U[1, 512] 193 -> 140 us, head_dim 256 118 -> 108 us).  A stage
+// then holds half the positions, and the two warps that share it take a head
+// each.  Everything after the streams sees one KV head with twice the query
+// heads.
 struct QuantArgs {
-  SplitArgs s;            // as for the 16-bit split kernel
+  SplitArgs s;            // as for the 16-bit split kernel; G and Hkv of HC heads as one
   const float* k_scales;  // [P][Hkv][PS]
   const float* v_scales;
+  int32_t G1, heads;      // query heads per KV head, KV heads
 };
 
-template <int D>
+template <int D, int NT8 = 1>
 struct QuantCfg {
-  static constexpr int kWarps = 4;
+  // Consumer warps: pairs that share a stage, 32 positions a warp, the pairs
+  // taking the stages in turn.  Turning codes into fragments is a long chain
+  // of short instructions, so each warp gets two independent blocks of 16
+  // positions, and there are as many pairs as the registers and the ring
+  // (whose stages every pair must return to) allow.
+  static constexpr int kWarps = NT8 == 2 && D <= 128 ? 4 : 6;
   static constexpr int kThreads = (kWarps + 1) * 32;
+  // CTAs of an SM: two, and one with twice the ring at D = 256, whose
+  // accumulators and fragments need more registers than two leave.
+  static constexpr int kCtas = D == 256 ? 1 : 2;
   static constexpr int kWidth = D < 128 ? D : 128;   // bytes of a swizzled row
   static constexpr int kTileBytes = kTile * D;       // K or V codes of a stage
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = 96 * 1024 / kStageBytes;  // 12, 6, 3
+  static constexpr int kStages = (192 / kCtas) * 1024 / kStageBytes;  // 12, 6, 6
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kSmemBytes = kRingBytes + 1024;
 };
 
-// Byte offset of (token t, 16-byte chunk c) in a tile of codes made of pieces
-// of 2^ps rows, each [D / kWidth][2^ps rows][kWidth] with the 128-byte (or at
-// D = 64 the 64-byte) swizzle.
-template <int D>
-__device__ __forceinline__ uint32_t code_offset(int t, int c, int ps) {
+// Byte offset of (token t, 16-byte chunk c) of a CTA's head in a tile of codes
+// made of pieces of 2^ps rows, each [D / kWidth][HC heads][2^ps rows][kWidth]
+// with the 128-byte (or at D = 64 the 64-byte) swizzle.
+template <int D, int HC>
+__device__ __forceinline__ uint32_t code_offset(int t, int c, int head, int ps) {
   constexpr int W = QuantCfg<D>::kWidth, kChunks = W / 16;
   const int rows = 1 << ps, r = t & (rows - 1);
   const int key = W == 128 ? (r & 7) : ((r >> 1) & 3);
-  return (uint32_t)((t >> ps) * (rows * D) + (c / kChunks) * (rows * W) + r * W +
-                    (((c % kChunks) ^ key) << 4));
-}
-
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
-  return __byte_perm(a, b, sel);
+  return (uint32_t)((t >> ps) * (rows * D * HC) + ((c / kChunks) * HC + head) * (rows * W) +
+                    r * W + (((c % kChunks) ^ key) << 4));
 }
 
 // log2 of a V scale for the running maximum; clamped, so that a zero row
@@ -75,12 +89,14 @@ __device__ __forceinline__ float scale_log2_of(float v) {
   return y;
 }
 
-// One consumer warp's 16 positions of a staged tile (K codes at kt, V codes
-// behind them, ks / vs the stage's scales): mma_block's counterpart.
-template <int D, int NT8>
+// One consumer warp's 32 positions of a staged tile (K codes at kt, V codes
+// behind them, ks / vs the scales of its positions), as two blocks of 16:
+// mma_block's counterpart.  They are the tile's positions t0.. of head `head`.
+// inside: every column attends all 32.
+template <int D, int NT8, int HC>
 __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, const float* vs_s,
-                                            int warp, int lane, int tok0, int lo, int hi,
-                                            const int (&col_lo)[NT8][2],
+                                            int t0, int head, int lane, int tok0, int lo, int hi,
+                                            bool inside, const int (&col_lo)[NT8][2],
                                             const int (&col_hi)[NT8][2],
                                             const uint32_t (&qf)[NT8][D / 16][2],
                                             const float (&col_scale)[NT8][2],
@@ -89,74 +105,93 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
   using H = ElemOps<__half>;
   const int gid = lane >> 2;
   const int mat = lane >> 3, mrow = lane & 7;
-  const int tok = 16 * warp + mrow + ((mat & 1) ? 8 : 0);  // matrix bit 0: tokens 8..15
-  const int half = mat >> 1;                               // matrix bit 1: dims 16..31
+  const int tok = t0 + mrow + ((mat & 1) ? 8 : 0);  // matrix bit 0: tokens 8..15 of a block
+  const int hd = mat >> 1;                          // matrix bit 1: dims 16..31
   const uint32_t kbase = smem_u32(kt);
   const uint32_t vbase = kbase + QuantCfg<D>::kTileBytes;
-  if (tok0 < lo || tok0 + 16 > hi) {
+  if (tok0 < lo || tok0 + 32 > hi) {
     // V codes outside the range become zeros: a zero weight meets no NaN
     uint8_t* vt = kt + QuantCfg<D>::kTileBytes;
-    for (int e = lane; e < 16 * (D / 16); e += 32) {
+    for (int e = lane; e < 32 * (D / 16); e += 32) {
       const int t = e / (D / 16), c = e % (D / 16);
       if (tok0 + t < lo || tok0 + t >= hi)
-        *reinterpret_cast<uint4*>(vt + code_offset<D>(16 * warp + t, c, ps)) =
+        *reinterpret_cast<uint4*>(vt + code_offset<D, HC>(t0 + t, c, head, ps)) =
             make_uint4(0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();
     __syncwarp();
   }
-  float sc[NT8][4];
+  float sc[2][NT8][4];
 #pragma unroll
-  for (int j = 0; j < NT8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
-  for (int kb = 0; kb < D / 32; ++kb) {
-    uint32_t r[4];  // (tokens 0-7, 8-15) x (dims 0-15, 16-31): four dims per register
-    ldmatrix_x4(r, kbase + code_offset<D>(tok, 2 * kb + half, ps));
+    for (int j = 0; j < NT8; ++j) sc[b][j][0] = sc[b][j][1] = sc[b][j][2] = sc[b][j][3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t af[4] = {e4m3_to_half2(r[2 * i] & 0xffffu),
-                              e4m3_to_half2(r[2 * i + 1] & 0xffffu),
-                              e4m3_to_half2(r[2 * i] >> 16), e4m3_to_half2(r[2 * i + 1] >> 16)};
+  for (int kb = 0; kb < D / 32; ++kb)
 #pragma unroll
-      for (int j = 0; j < NT8; ++j) H::mma(sc[j], af, qf[j][2 * kb + i][0], qf[j][2 * kb + i][1]);
+    for (int b = 0; b < 2; ++b) {
+      uint32_t r[4];  // (tokens 0-7, 8-15) x (dims 0-15, 16-31): four dims per register
+      ldmatrix_x4(r, kbase + code_offset<D, HC>(tok + 16 * b, 2 * kb + hd, head, ps));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t af[4] = {e4m3_to_half2(r[2 * i] & 0xffffu),
+                                e4m3_to_half2(r[2 * i + 1] & 0xffffu),
+                                e4m3_to_half2(r[2 * i] >> 16), e4m3_to_half2(r[2 * i + 1] >> 16)};
+#pragma unroll
+        for (int j = 0; j < NT8; ++j)
+          H::mma(sc[b][j], af, qf[j][2 * kb + i][0], qf[j][2 * kb + i][1]);
+      }
     }
+  // this lane's positions: gid + 8 i of the 32
+  float ks[4], vs[4], lv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ks[i] = ks_s[gid + 8 * i];
+    vs[i] = vs_s[gid + 8 * i];
+    lv[i] = scale_log2_of(vs[i]);
   }
-  const int tok_a = tok0 + gid, tok_b = tok0 + gid + 8;
-  const float ks_a = ks_s[16 * warp + gid], ks_b = ks_s[16 * warp + gid + 8];
-  const float vs_a = vs_s[16 * warp + gid], vs_b = vs_s[16 * warp + gid + 8];
-  const float lv_a = scale_log2_of(vs_a), lv_b = scale_log2_of(vs_b);
-  uint32_t pb_hi[NT8][2], pb_lo[NT8][2];
+  uint32_t pb_hi[2][NT8][2], pb_lo[2][NT8][2];
   bool rescale = false;
   float alpha[NT8][2];
 #pragma unroll
   for (int j = 0; j < NT8; ++j) {
-    float w[4];
+    float w[4][2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const bool in_a = tok_a >= col_lo[j][e] && tok_a < col_hi[j][e];
-      const bool in_b = tok_b >= col_lo[j][e] && tok_b < col_hi[j][e];
-      const float sa = in_a ? sc[j][e] * (col_scale[j][e] * ks_a) : -INFINITY;
-      const float sb = in_b ? sc[j][e + 2] * (col_scale[j][e] * ks_b) : -INFINITY;
-      float mx = fmaxf(in_a ? sa + lv_a : -INFINITY, in_b ? sb + lv_b : -INFINITY);
+      float sv[4], mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sv[i] = sc[i >> 1][j][e + 2 * (i & 1)] * (col_scale[j][e] * ks[i]);
+        if (!inside) {
+          const int t = tok0 + gid + 8 * i;
+          if (t < col_lo[j][e] || t >= col_hi[j][e]) sv[i] = -INFINITY;
+        }
+        mx = fmaxf(mx, sv[i] + (inside || sv[i] != -INFINITY ? lv[i] : 0.f));
+      }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       const float m_new = fmaxf(m_run[j][e], mx);
       alpha[j][e] = (m_new == -INFINITY) ? 1.f : fast_exp2(m_run[j][e] - m_new);
       rescale |= alpha[j][e] != 1.f;
-      const float pa = in_a ? fast_exp2(sa - m_new) : 0.f;
-      const float pb = in_b ? fast_exp2(sb - m_new) : 0.f;
-      l_part[j][e] = l_part[j][e] * alpha[j][e] + pa + pb;
+      float l = l_part[j][e] * alpha[j][e];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = inside || sv[i] != -INFINITY;
+        const float p = in ? fast_exp2(sv[i] - m_new) : 0.f;
+        l += p;
+        w[i][e] = in ? p * vs[i] : 0.f;
+      }
+      l_part[j][e] = l;
       m_run[j][e] = m_new;
-      w[e] = in_a ? pa * vs_a : 0.f;
-      w[e + 2] = in_b ? pb * vs_b : 0.f;
     }
-    const uint32_t h0 = H::pack2(w[0], w[1]), h1 = H::pack2(w[2], w[3]);
-    const float2 f0 = H::unpack2(h0), f1 = H::unpack2(h1);
-    pb_hi[j][0] = movmatrix_trans(h0);
-    pb_hi[j][1] = movmatrix_trans(h1);
-    pb_lo[j][0] = movmatrix_trans(H::pack2(w[0] - f0.x, w[1] - f0.y));
-    pb_lo[j][1] = movmatrix_trans(H::pack2(w[2] - f1.x, w[3] - f1.y));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = H::pack2(w[i][0], w[i][1]);
+      const float2 f = H::unpack2(h);
+      pb_hi[i >> 1][j][i & 1] = movmatrix_trans(h);
+      pb_lo[i >> 1][j][i & 1] = movmatrix_trans(H::pack2(w[i][0] - f.x, w[i][1] - f.y));
+    }
   }
   if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -172,23 +207,25 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
   // out^T += V^T . W^T: row gid of a tile of 16 dims is dim 2 gid, row gid + 8
   // dim 2 gid + 1
 #pragma unroll
-  for (int kb = 0; kb < D / 32; ++kb) {
-    uint32_t r[4];  // as for K, transposed: (2 tokens x 2 dims) per register
-    ldmatrix_x4_trans(r, vbase + code_offset<D>(tok, 2 * kb + half, ps));
+  for (int kb = 0; kb < D / 32; ++kb)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t a0 = e4m3_to_half2(r[2 * i] & 0xffffu), a1 = e4m3_to_half2(r[2 * i] >> 16);
-      const uint32_t b0 = e4m3_to_half2(r[2 * i + 1] & 0xffffu),
-                     b1 = e4m3_to_half2(r[2 * i + 1] >> 16);
-      const uint32_t af[4] = {byte_perm(a0, a1, 0x5410), byte_perm(a0, a1, 0x7632),
-                              byte_perm(b0, b1, 0x5410), byte_perm(b0, b1, 0x7632)};
+    for (int b = 0; b < 2; ++b) {
+      uint32_t r[4];  // as for K, transposed: (2 tokens x 2 dims) per register
+      ldmatrix_x4_trans(r, vbase + code_offset<D, HC>(tok + 16 * b, 2 * kb + hd, head, ps));
 #pragma unroll
-      for (int j = 0; j < NT8; ++j) {
-        H::mma(acc[2 * kb + i][j], af, pb_hi[j][0], pb_hi[j][1]);
-        H::mma(acc[2 * kb + i][j], af, pb_lo[j][0], pb_lo[j][1]);
+      for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0u, 0x3120);  // (2 dims x 2 tokens)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t af[4] = {e4m3_to_half2(r[2 * i] & 0xffffu), e4m3_to_half2(r[2 * i] >> 16),
+                                e4m3_to_half2(r[2 * i + 1] & 0xffffu),
+                                e4m3_to_half2(r[2 * i + 1] >> 16)};
+#pragma unroll
+        for (int j = 0; j < NT8; ++j) {
+          H::mma(acc[2 * kb + i][j], af, pb_hi[b][j][0], pb_hi[b][j][1]);
+          H::mma(acc[2 * kb + i][j], af, pb_lo[b][j][0], pb_lo[b][j][1]);
+        }
       }
     }
-  }
 }
 
 // A row of q as fp16 fragments, 4 consecutive dims per lane and 16-dim step;
@@ -230,12 +267,15 @@ __device__ __forceinline__ float load_q_row(const uint16_t* row, bool live, int 
 }
 
 // CL: a cluster plan, as in split_mma_body.
-template <int D, int NT8, class E, bool CL>
-__global__ void __launch_bounds__(QuantCfg<D>::kThreads)
+template <int D, int NT8, class E, bool CL, int HC>
+__global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::kCtas)
     quant_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const QuantArgs qa) {
-  using C = QuantCfg<D>;
+  using C = QuantCfg<D, NT8>;
+  constexpr int kPairs = C::kWarps / 2;
+  static_assert(C::kStages % kPairs == 0, "a pair sees every phase of its stages");
   constexpr int KS = D / 16, kWarps = C::kWarps, GP = 8 * NT8;
+  constexpr int kStagePos = kTile / HC;
   const SplitArgs& a = qa.s;
 
   __shared__ __align__(8) uint64_t full_bar[C::kStages];
@@ -245,7 +285,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
   __shared__ int32_t coord_s[kMaxPieces];
   __shared__ float2 ml_s[kWarps][GP];
   __shared__ float cw_s[kWarps][GP];
-  __shared__ float2 row_s[GP];
+  __shared__ float2 row_s[GP * HC];
   __shared__ int32_t bad_s;
   __shared__ volatile int32_t abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -257,7 +297,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
     for (int st = 0; st < C::kStages; ++st) {
       // the boxes' arrival, and one of each producer lane for its scales
       mbar_init(smem_u32(&full_bar[st]), 1 + 32);
-      mbar_init(smem_u32(&empty_bar[st]), kWarps);
+      mbar_init(smem_u32(&empty_bar[st]), 2);
     }
     if constexpr (CL) mbar_init(smem_u32(&recv_bar), cluster_size());
     fence_mbar_init();
@@ -289,7 +329,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
   }
   const SeqRange r = seq_range(ld_global_s32(a.seq_lens + b), a.window, capacity, a.chunk,
                                a.max_shards, a.T, a.balanced);
-  const int R = a.T * a.G;
+  const int R = a.T * a.G, R1 = a.T * qa.G1;  // query rows of the CTA, of one head
   const int gid = lane >> 2, tig = lane & 3;
   uint8_t* recv = ring + C::kRingBytes;
 
@@ -306,7 +346,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
         cluster_finish<D, E>(a, x, b, h, smem_u32(&recv_bar), recv, kWarps * 32);
       }
     } else if (s == 0) {
-      zero_group_rows<D, GP>(a, b, h);
+      zero_group_rows<D, GP * HC>(a, b, h);
     }
     return;
   }
@@ -314,8 +354,8 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
   const int shard_lo = r.base + s * r.chunk;
   const int lo = max(r.start, shard_lo);
   const int hi = min(r.end, shard_lo + r.chunk);
-  const int n_tiles = (hi - shard_lo + kTile - 1) / kTile;
-  const int pieces = kTile / box_t, n_pieces = n_tiles * pieces;
+  const int n_tiles = (hi - shard_lo + kStagePos - 1) / kStagePos;
+  const int pieces = kStagePos / box_t, n_pieces = n_tiles * pieces;
 
   if (warp == kWarps) {
     const int pool_rows = a.num_pages * a.page_size;  // past the pool: zeros
@@ -347,8 +387,10 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
         raise_error(a.err, DECODE_ATTN_DEV_BAD_PAGE);
       }
       __syncwarp();
-      mbar_arrive(smem_u32(&full_bar[0]));
-      if (lane == 0) mbar_arrive(smem_u32(&full_bar[0]));
+      for (int i = 0; i < kPairs; ++i) {  // each pair's first stage
+        mbar_arrive(smem_u32(&full_bar[i]));
+        if (lane == 0) mbar_arrive(smem_u32(&full_bar[i]));
+      }
       return;
     }
     __syncwarp();
@@ -360,7 +402,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
       if (i >= C::kStages) {
         int go = 1;
         if (lane == 0) {
-          if (!mbar_wait(smem_u32(&empty_bar[st]), ((i / C::kStages) & 1) ^ 1)) {
+          if (!mbar_wait_hot(smem_u32(&empty_bar[st]), ((i / C::kStages) & 1) ^ 1)) {
             abort_s = 1;
             raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
           }
@@ -373,24 +415,26 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
       __syncwarp();
       if (lane < 2 * pieces) {  // at most 16 boxes: pieces of 8 positions or more
         const int coord = coord_s[i * pieces + (lane >> 1)];
-        const bool in = PGD_IN(coord == pool_rows ? 0 : (int64_t)coord + box_t - 1, pool_rows, a.err);
+        const bool in =
+            PGD_IN(coord == pool_rows ? 0 : (int64_t)coord + box_t - 1, pool_rows, a.err);
         tma_load_4d_hint(smem_u32(ring + st * C::kStageBytes) + (lane & 1) * C::kTileBytes +
-                             (lane >> 1) * box_t * D,
-                         (lane & 1) ? &tmap_v : &tmap_k, 0, in ? coord : pool_rows, h, 0, fb,
-                         policy);
+                             (lane >> 1) * box_t * D * HC,
+                         (lane & 1) ? &tmap_v : &tmap_k, 0, in ? coord : pool_rows, h * HC, 0,
+                         fb, policy);
       }
       {
-        // this lane's 4 positions' scales (lanes 0-15 K, 16-31 V); zeros
-        // where no position is attended
-        const int t = 4 * (lane & 15);
+        // this lane's 4 positions' scales (lanes 0-15 K, 16-31 V; of 16 lanes
+        // the upper 8 the second head's); zeros where no position is attended
+        const int t = 4 * (lane & (kStagePos / 4 - 1));
+        const int hd = h * HC + (HC == 2 ? (lane >> 3) & 1 : 0);
         const int coord = coord_s[i * pieces + t / box_t];
         const bool in = coord < pool_rows;
         const int row = (in ? coord : 0) + (in ? t % box_t : 0);
-        const size_t at = ((size_t)(row >> a.page_shift) * a.Hkv + h) * a.page_size +
+        const size_t at = ((size_t)(row >> a.page_shift) * qa.heads + hd) * a.page_size +
                           (row & (a.page_size - 1));
-        const bool ok = PGD_IN(at + 3, (size_t)pool_rows * a.Hkv, a.err);
+        const bool ok = PGD_IN(at + 3, (size_t)pool_rows * qa.heads, a.err);
         asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         smem_u32(&scale_s[st][lane >> 4][t])),
+                         smem_u32(&scale_s[st][lane >> 4][4 * (lane & 15)])),
                      "l"(scales + (ok ? at : 0)), "r"(in && ok ? 16 : 0)
                      : "memory");
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
@@ -399,7 +443,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
     }
     // this CTA's copies in flight have landed before the warp exits
     for (int i = max(0, issued - C::kStages); i < issued; ++i)
-      mbar_wait(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1);
+      mbar_wait_hot(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1);
     return;
   }
 
@@ -408,19 +452,25 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
   float acc[KS][NT8][4];
   int col_lo[NT8][2], col_hi[NT8][2];
   float m_run[NT8][2], l_part[NT8][2], col_scale[NT8][2];
+  // this warp's positions of a stage, or head of the CTA
+  const int half = warp & 1, head = HC == 2 ? half : 0;
+  // query row rr of the head (token rr / G1) among the CTA's rows
+  auto cta_row = [&](int rr, int hd) {
+    return HC == 1 ? rr : rr / qa.G1 * a.G + hd * qa.G1 + rr % qa.G1;
+  };
 #pragma unroll
   for (int j = 0; j < NT8; ++j) {
     const int rr = 8 * j + gid;
-    size_t qr = group_row(b, h, rr < R ? rr : 0, a.T, a.G, a.Hq);
+    size_t qr = group_row(b, h, cta_row(rr < R1 ? rr : 0, head), a.T, a.G, a.Hq);
     if (!PGD_IN(qr, (size_t)a.batch * a.T * a.Hq, a.err)) qr = 0;
     const float f =
-        load_q_row<D, E>(static_cast<const uint16_t*>(a.q) + qr * D, rr < R, tig, qf[j]);
+        load_q_row<D, E>(static_cast<const uint16_t*>(a.q) + qr * D, rr < R1, tig, qf[j]);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       // this lane's score columns are rows 8j + 2 tig + e
       col_scale[j][e] = a.scale_log2 * __shfl_sync(0xffffffffu, f, (2 * tig + e) * 4);
       const int cr = 8 * j + 2 * tig + e;
-      const int t = cr < R ? cr / a.G : a.T - 1;
+      const int t = cr < R1 ? cr / qa.G1 : a.T - 1;
       col_hi[j][e] = r.end - a.T + t + 1;
       col_lo[j][e] = a.window > 0 ? max(0, col_hi[j][e] - a.window) : 0;
       m_run[j][e] = -INFINITY;
@@ -434,19 +484,23 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[mi][j][e] = 0.f;
   const int piece_shift = __ffs(box_t) - 1;
-  for (int i = 0; i < n_tiles; ++i) {
+  // positions that every query row attends
+  const int in_hi = r.end - a.T + 1, in_lo = a.window > 0 ? r.end - a.window : 0;
+  for (int i = warp >> 1; i < n_tiles; i += kPairs) {
     const int st = i % C::kStages;
-    if (!mbar_wait(smem_u32(&full_bar[st]), (i / C::kStages) & 1)) {
+    if (!mbar_wait_hot(smem_u32(&full_bar[st]), (i / C::kStages) & 1)) {
       abort_s = 1;
       raise_error(a.err, DECODE_ATTN_DEV_TIMEOUT);
       break;
     }
     if (bad_s || abort_s) break;
-    const int tok0 = shard_lo + i * kTile + 16 * warp;
-    if (tok0 + 16 > lo && tok0 < hi)
-      quant_block<D, NT8>(ring + st * C::kStageBytes, scale_s[st][0], scale_s[st][1], warp, lane,
-                          tok0, lo, hi, col_lo, col_hi, qf, col_scale, acc, m_run, l_part,
-                          piece_shift);
+    const int t0 = HC == 1 ? 32 * half : 0;
+    const int tok0 = shard_lo + i * kStagePos + t0;
+    if (tok0 + 32 > lo && tok0 < hi)
+      quant_block<D, NT8, HC>(ring + st * C::kStageBytes, &scale_s[st][0][32 * half],
+                              &scale_s[st][1][32 * half], t0, head, lane, tok0, lo, hi,
+                              tok0 >= max(lo, in_lo) && tok0 + 32 <= min(hi, in_hi), col_lo,
+                              col_hi, qf, col_scale, acc, m_run, l_part, piece_shift);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));
   }
@@ -463,7 +517,8 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
       l_part[j][e] = l;
     }
   named_barrier_sync(1, kWarps * 32);  // every consumer is done with the ring
-  constexpr int kRowStride = D + 4;
+  // the padding sends a fragment's stores to distinct banks, where it fits
+  constexpr int kRowStride = kWarps * GP * (D + 4) * 4 <= C::kRingBytes ? D + 4 : D;
   static_assert(kWarps * GP * kRowStride * 4 <= C::kRingBytes, "warp states fit in the ring");
   float* acc_s = reinterpret_cast<float*>(ring);
   if (gid == 0) {
@@ -485,20 +540,30 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
           make_float2(acc[mi][j][1], acc[mi][j][3]);
     }
   named_barrier_sync(1, kWarps * 32);
+  // the CTA's row r: its head and the row among the head's
+  auto head_row = [&](int r, int& hd) {
+    if (HC == 1) {
+      hd = 0;
+      return r;
+    }
+    hd = r % a.G / qa.G1;
+    return r / a.G * qa.G1 + r % qa.G1;
+  };
   if (threadIdx.x < R) {
-    const int g = threadIdx.x;
+    int hd;
+    const int g = head_row(threadIdx.x, hd);
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml_s[w][g].x);
+    for (int w = 0; w < kWarps; w += HC) M = fmaxf(M, ml_s[w + hd][g].x);
     float L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = ml_s[w][g];
+    for (int w = 0; w < kWarps; w += HC) {
+      const float2 ml = ml_s[w + hd][g];
       const float c = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
       if (ml.y != 0.f) L += c * ml.y;
-      cw_s[w][g] = c;
+      cw_s[w + hd][g] = c;
     }
-    row_s[g] = make_float2(M, L);
+    row_s[threadIdx.x] = make_float2(M, L);
   }
   named_barrier_sync(1, kWarps * 32);
   const bool dead = bad_s != 0 || abort_s != 0;
@@ -509,20 +574,23 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
   }
   constexpr int kQuads = D / 4;
   for (int e = threadIdx.x; e < R * kQuads; e += kWarps * 32) {
-    const int g = e / kQuads, q = e % kQuads;
-    const float2 ML = row_s[g];
+    const int rc = e / kQuads, q = e % kQuads;
+    int hd;
+    const int g = head_row(rc, hd);
+    const float2 ML = row_s[rc];
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float c = cw_s[w][g];
+    for (int w = 0; w < kWarps; w += HC) {
+      const float c = cw_s[w + hd][g];
       if (c == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(acc_s + (w * GP + g) * kRowStride + 4 * q);
+      const float4 v =
+          *reinterpret_cast<const float4*>(acc_s + ((w + hd) * GP + g) * kRowStride + 4 * q);
       O.x += c * v.x;
       O.y += c * v.y;
       O.z += c * v.z;
       O.w += c * v.w;
     }
-    const size_t row = group_row(b, h, g, a.T, a.G, a.Hq);
+    const size_t row = group_row(b, h, rc, a.T, a.G, a.Hq);
     if (!a.split) {
       if (!PGD_IN(row, (size_t)a.batch * a.T * a.Hq, a.err)) continue;
       const bool z = dead || ML.y == 0.f;
@@ -535,7 +603,7 @@ __global__ void __launch_bounds__(QuantCfg<D>::kThreads)
     const float2 MLw = make_float2(ML.x, dead ? -1.f : ML.y);
     if constexpr (CL) {
       x.push(e, Ow);
-      if (q == 0) x.push_ml(g, MLw);
+      if (q == 0) x.push_ml(rc, MLw);
     } else {
       const size_t slot = row * a.max_shards + s;
       if (!PGD_IN(slot, (size_t)a.batch * a.T * a.Hq * a.max_shards, a.err)) continue;

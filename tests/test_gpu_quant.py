@@ -202,6 +202,31 @@ def test_quant_same_bits_every_run_and_beside_decode(pkg):
         assert err == 0 and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D,PS,window", [
+    (1, 8, 2, 64, 8, 0), (1, 8, 2, 64, 16, 100), (1, 32, 4, 128, 16, 0), (1, 8, 2, 128, 8, 0),
+    (2, 8, 2, 64, 32, 0), (3, 4, 2, 128, 16, 70), (1, 6, 2, 256, 8, 0), (1, 4, 4, 64, 64, 0),
+])
+def test_quant_two_heads_per_cta(pkg, T, Hq, Hkv, D, PS, window):
+    """Small boxes and a step that the bound on the lengths calls large: the
+    plan takes two KV heads per CTA.  Short and empty sequences among them."""
+    cap = 65536 // PS * 8
+    d = cache(450, [900, 1, 0, 77, 2300, 64], T, Hq=Hq, Hkv=Hkv, D=D, PS=PS, dtype=BF16,
+              max_pages=cap)
+    p = pkg.DecodeAttnParams(6, Hq, Hkv, D, PS, cap, d["k_pages"].shape[0], 0, 1.0, window, 0, 0,
+                             0, T, 1, 0)
+    plan = pkg.decode_attn_quant_make_plan(p, 152)
+    heads = plan.grid_x if plan.head_fastest else plan.grid_y
+    assert heads == Hkv // 2 or window
+    check(pkg, d, T, window)
+    check(pkg, d, T, window, force_chunk=256)  # shards and their merge
+    d["table"] = d["table"].clone()
+    d["table"][4, 20] = -3
+    got, err = run(pkg, d, T, window)
+    bad = 20 * PS + PS > (max(0, 2300 - T + 1 - window) if window else 0)
+    assert err == (pkg.DEV_BAD_PAGE if bad else 0)
+    assert torch.all(got[4 * T:5 * T] == 0) == bad
+
+
 def test_quant_long_context(pkg):
     d = cache(439, [40000], 1, Hq=8, Hkv=1, D=128, PS=64, dtype=F16)
     check(pkg, d, 1, max_seq_len=40000)
