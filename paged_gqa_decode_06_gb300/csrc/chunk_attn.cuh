@@ -80,10 +80,23 @@ struct __align__(8) ChunkBars {
   uint64_t v_edge, v_clean;   // an edge tile's V has landed; is looked over
 };
 
+// One CTA's share of the work, found from its slot.
+struct ChunkItem {
+  int32_t b, t0, t1;     // sequence, its query tokens [t0, t1)
+  int32_t row0;          // row of t0 among all tokens
+  int32_t p0;            // position of t0
+  int32_t lo, hi;        // keys that some query of the item attends
+  int32_t base, tiles;   // first key of the first tile, number of key tiles
+  int32_t shards;        // CTAs that share the tiles (0: nothing to attend)
+  int32_t status;
+  bool any;              // the slot holds query tokens
+};
+
 // What the CTA shares beside Q and the ring.
 template <int kRing, int kStreams, int kKeys, int kMaxEdges>
 struct ChunkShared {
   ChunkBars<kRing, kStreams, kKeys / 64> bar;
+  ChunkItem item;
   uint32_t tmem;
   int32_t abort;
   int32_t bad_lo, bad_hi;  // positions in pages outside the pool
@@ -112,28 +125,32 @@ struct ChunkCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 };
 
-// One CTA's share of the work, found from its slot.
-struct ChunkItem {
-  int32_t b, t0, t1;     // sequence, its query tokens [t0, t1)
-  int32_t row0;          // row of t0 among all tokens
-  int32_t p0;            // position of t0
-  int32_t lo, hi;        // keys that some query of the item attends
-  int32_t base, tiles;   // first key of the first tile, number of key tiles
-  int32_t shards;        // CTAs that share the tiles (0: nothing to attend)
-  int32_t status;
-  bool any;              // the slot holds query tokens
-};
-
 // Sequence b owns the slots [offsets[b] / item_tok + b, offsets[b+1] /
 // item_tok + b + 1): at least the tiles it needs, and an ascending function
 // of b, so a slot finds its sequence by search.
 template <int KT>
 __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, int lane) {
   ChunkItem it{};
-  auto first_slot = [&](int b) { return (int64_t)(a.offsets[b] / a.item_tok) + b; };
-  const int b = warp_search(a.B, slot, lane, first_slot);
-  if (b < 0) return it;
-  const RowRange r = row_range(a.offsets, b, a.total);
+  int b;
+  RowRange r;
+  int32_t L = 0;
+  if (a.B < 32) {  // one round trip: every offset and length at once
+    const int32_t off = lane <= a.B ? ld_global_s32(a.offsets + lane) : 0;
+    const int32_t len = lane < a.B ? ld_global_s32(a.seq_lens + lane) : 0;
+    b = __popc(__ballot_sync(0xffffffffu, lane < a.B && off / a.item_tok + lane <= slot)) - 1;
+    if (b < 0) return it;
+    const int32_t z = __shfl_sync(0xffffffffu, off, b + 1);
+    r.first = __shfl_sync(0xffffffffu, off, b);
+    r.ok = r.first >= 0 && r.first <= z && z <= a.total;
+    r.count = r.ok ? z - r.first : 0;
+    L = __shfl_sync(0xffffffffu, len, b);
+  } else {
+    b = warp_search(a.B, slot, lane,
+                    [&](int i) { return (int64_t)(a.offsets[i] / a.item_tok) + i; });
+    if (b < 0) return it;
+    r = row_range(a.offsets, b, a.total);
+    L = ld_global_s32(a.seq_lens + b);
+  }
   it.b = b;
   if (!r.ok) {
     it.status = DECODE_ATTN_DEV_BAD_LEN;
@@ -145,7 +162,6 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, in
   it.t0 = (int32_t)t0;
   it.t1 = min(r.count, it.t0 + a.item_tok);
   it.row0 = r.first + it.t0;
-  const int32_t L = ld_global_s32(a.seq_lens + b);
   if (L < 0 || L > a.max_pages * a.page_size) {
     it.status = DECODE_ATTN_DEV_BAD_LEN;
     return it;
@@ -164,6 +180,20 @@ template <class E>
 __device__ __forceinline__ uint32_t wild2(uint32_t w) {
   constexpr uint32_t kExp = std::is_same<E, __nv_bfloat16>::value ? 0x7f807f80u : 0x7c007c00u;
   return __vcmpeq2(w & kExp, kExp);
+}
+
+// Larger magnitude of each of two 16-bit values; NaN if either is.
+template <class E>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+    const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<__nv_bfloat162*>(&a)),
+                                         __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  } else {
+    const __half2 m = __hmax2_nan(__habs2(*reinterpret_cast<__half2*>(&a)),
+                                  __habs2(*reinterpret_cast<__half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
 }
 
 // The lowest n bits, for any n.
@@ -339,7 +369,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const int shard = (blockIdx.x / a.Hkv) % a.max_shards;
   // the last tiles of a sequence see the most keys: they start first
   const int slot = a.slots - 1 - blockIdx.x / (a.Hkv * a.max_shards);
-  const ChunkItem it = chunk_item<KT>(a, slot, lane);
+  // The issuing warp allocates the tensor memory while the others look for
+  // their item, and takes it from them.
+  constexpr int kOthers = NS * 128 + 32;  // the row threads and the issuing warp
+  ChunkItem it{};
+  if (warp == kMma) {
+    tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
+    tc_fence_before();
+  } else {
+    it = chunk_item<KT>(a, slot, lane);
+  }
+  if (threadIdx.x == 0) sh.item = it;
+  if (warp < kProducer || warp == kMma) {
+    named_barrier_sync(1, kOthers);
+    tc_fence_after();
+  }
+  if (warp == kMma) {
+    it = sh.item;
+    if (!it.any || shard >= it.shards) tmem_free(sh.tmem, C::kTmemCols);
+  }
   if (blockIdx.x == 0)  // offsets that no slot may lead to are checked once
     for (int b = threadIdx.x; b < a.B; b += C::kThreads)
       if (!row_range(a.offsets, b, a.total).ok) raise_error(a.err, DECODE_ATTN_DEV_BAD_LEN);
@@ -370,10 +418,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   };
 
   // two streams: 384 threads launched with 168 registers each; the row threads
-  // (128 scores apiece) take 216, the last warpgroup 72
-  constexpr int kOthers = NS * 128 + 32;  // the row threads and the issuing warp
+  // (128 scores apiece) take 200, the last warpgroup 104
   if (warp >= kProducer) {
-    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kProducer) {
       if (lane == 0) {
         const uint32_t qb = smem_u32(&bar.q_full);
@@ -437,10 +484,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
 
     if (warp == kMma) {
-      tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
-      tc_fence_before();
-      named_barrier_sync(1, kOthers);
-      tc_fence_after();
       // One thread waits for and issues everything: the pace of this loop is
       // the pace of the tensor cores (with warp-wide waits and votes a unit
       // took 2000 cycles, of which the products need 1100).
@@ -465,32 +508,34 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       const int k0 = key0 + j * KT;
       uint8_t* vt = ring + ((2 * j + 1) % NR) * C::kTileBytes;
       if (warp == kMma + 1 && lane == 0 && edges < C::kMaxEdges) sh.edge_key[edges] = k0;
-      // a quick pass: whether any value of the tile needs a look at all
       const int first = (warp - kMma - 1) * 32 + lane;
-      bool look = k0 < it.lo || k0 + KT > it.hi;
-      if (!look) {
-        uint32_t any = 0;
-#pragma unroll 8
+      uint4* tile = reinterpret_cast<uint4*>(vt);
+      auto key_of = [&](int e) {  // groups of 8 keys, 1 KB per 64 dims
+        return k0 + e / D * 8 + (e % 64) / 8;
+      };
+      // keys outside the range: whole groups of 8 and what is left of one
+      if (k0 < it.lo || k0 + KT > it.hi)
         for (int e = first; e < C::kTileBytes / 16; e += 64) {
-          const uint4 v = reinterpret_cast<const uint4*>(vt)[e];
-          any |= wild2<E>(v.x) | wild2<E>(v.y) | wild2<E>(v.z) | wild2<E>(v.w);
+          const int key = key_of(e);
+          if (key < it.lo || key >= it.hi) tile[e] = make_uint4(0u, 0u, 0u, 0u);
         }
-        look = any != 0;
+      // the largest magnitude of this thread's values, NaN if there is one
+      uint32_t top = 0;
+#pragma unroll 8
+      for (int e = first; e < C::kTileBytes / 16; e += 64) {
+        const uint4 v = tile[e];
+        top = max2_nan<E>(max2_nan<E>(top, v.x), max2_nan<E>(v.y, max2_nan<E>(v.z, v.w)));
       }
-      for (int e = first; look && e < C::kTileBytes / 16; e += 64) {
-        const int t = e / D * 8 + (e % 64) / 8;  // groups of 8 tokens, 1 KB per 64 dims
-        uint4* at = reinterpret_cast<uint4*>(vt) + e;
-        if (k0 + t < it.lo || k0 + t >= it.hi) {
-          *at = make_uint4(0u, 0u, 0u, 0u);
-          continue;
+      if (wild2<E>(top) != 0u)
+        for (int e = first; e < C::kTileBytes / 16; e += 64) {
+          const uint4 v = tile[e];
+          const uint4 m = make_uint4(wild2<E>(v.x), wild2<E>(v.y), wild2<E>(v.z), wild2<E>(v.w));
+          if ((m.x | m.y | m.z | m.w) == 0u) continue;
+          tile[e] = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
+          const int t = key_of(e) - k0;
+          if (edges < C::kMaxEdges) atomicOr(&sh.wild[edges][t / 32], 1u << (t & 31));
+          sh.wild_any = 1;
         }
-        const uint4 v = *at;
-        const uint4 m = make_uint4(wild2<E>(v.x), wild2<E>(v.y), wild2<E>(v.z), wild2<E>(v.w));
-        if ((m.x | m.y | m.z | m.w) == 0u) continue;
-        *at = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
-        if (edges < C::kMaxEdges) atomicOr(&sh.wild[edges][t / 32], 1u << (t & 31));
-        sh.wild_any = 1;
-      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar.v_clean));
@@ -500,9 +545,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   }
 
   // ---------------------------------------------------------- softmax rows
-  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-  named_barrier_sync(1, kOthers);  // the tensor memory is there
-  tc_fence_after();
+  if constexpr (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
   const uint32_t tmem = sh.tmem, tmem_o = tmem + 2 * KT;  // O after the two S buffers
   const int s = warp >> 2;
   if (s < ns) {
@@ -610,10 +653,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     // rows that attend a page outside the pool are zeroed
     const bool dead =
         !ok || (pos >= sh.bad_lo && (a.window <= 0 || pos - a.window + 1 < sh.bad_hi));
-    const size_t orow = (size_t)(it.row0 + s * a.tile_tok + tok) * a.Hq + (size_t)h * a.G +
-                        row % a.G;
-    const bool in = tok < a.tile_tok && it.t0 + s * a.tile_tok + tok < te &&
-                    PGD_IN(orow, (size_t)a.total * a.Hq, a.err);
+    // this row among the CTA's output rows, or -1
+    const size_t row_base = (size_t)it.row0 * a.Hq + (size_t)h * a.G;
+    int rel = (s * a.tile_tok + tok) * a.Hq + row % a.G;
+    if (tok >= a.tile_tok || it.t0 + s * a.tile_tok + tok >= te ||
+        !PGD_IN(row_base + rel, (size_t)a.total * a.Hq, a.err))
+      rel = -1;
     // V rows with a NaN or Inf reach the rows that attend them
     auto patch = [&](int c, float (&o)[32]) {
       for (int e = 0; e < C::kMaxEdges; ++e)
@@ -637,33 +682,61 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           }
         }
     };
+    // A thread holds a row, so its stores would touch 32 rows at a time; 128
+    // bytes of each of the warp's rows go through shared memory instead (this
+    // stream's Q, which no product needs any more; 16-byte chunk c of row r at
+    // c ^ (r & 7)) and out as whole lines, 8 lanes a row.
     const bool whole = it.shards == 1;
     const float inv = dead || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-    const size_t slot_w = orow * a.max_shards + shard;
-    if (!whole && in) a.ws_ml[slot_w] = make_float2(m, dead ? -1.f : l);
-#pragma unroll
-    for (int c = 0; c < D; c += 32) {
-      float o[32];
-      tmem_ld32(o, tmem_o + s * D + lanes + c);
-      tmem_wait_ld();
-      if (!in) continue;
-      if (sh.wild_any) patch(c, o);
+    if (!whole && rel >= 0)
+      a.ws_ml[(row_base + rel) * a.max_shards + shard] = make_float2(m, dead ? -1.f : l);
+    uint4* stage = reinterpret_cast<uint4*>(smem + s * C::kQBytes) + (warp & 3) * 256;
+    const int step = whole ? 64 : 32;  // columns of 128 bytes
+    for (int c = 0; c < D; c += step) {
       if (whole) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * D + c);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
+        for (int k = 0; k < 2; ++k) {
+          float o[32];
+          tmem_ld32(o, tmem_o + s * D + lanes + c + 32 * k);
+          tmem_wait_ld();
+          if (sh.wild_any && rel >= 0) patch(c + 32 * k, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(ElemOps<E>::pack2(o[8 * i], o[8 * i + 1]),
-                              ElemOps<E>::pack2(o[8 * i + 2], o[8 * i + 3]),
-                              ElemOps<E>::pack2(o[8 * i + 4], o[8 * i + 5]),
-                              ElemOps<E>::pack2(o[8 * i + 6], o[8 * i + 7]));
-      } else if (!dead) {
-        float4* dst = reinterpret_cast<float4*>(a.ws_acc + slot_w * D + c);
+          for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            stage[lane * 8 + ((4 * k + i) ^ (lane & 7))] =
+                make_uint4(ElemOps<E>::pack2(o[8 * i], o[8 * i + 1]),
+                           ElemOps<E>::pack2(o[8 * i + 2], o[8 * i + 3]),
+                           ElemOps<E>::pack2(o[8 * i + 4], o[8 * i + 5]),
+                           ElemOps<E>::pack2(o[8 * i + 6], o[8 * i + 7]));
+        }
+      } else {
+        float o[32];
+        tmem_ld32(o, tmem_o + s * D + lanes + c);
+        tmem_wait_ld();
+        if (sh.wild_any && rel >= 0) patch(c, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          stage[lane * 8 + (i ^ (lane & 7))] =
+              make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                         __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
       }
+      __syncwarp();
+      const int chunk = lane & 7;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const uint4 v = stage[r * 8 + (chunk ^ (r & 7))];
+        const int to = __shfl_sync(0xffffffffu, rel, r);
+        if (to < 0) continue;
+        if (whole)
+          reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (row_base + to) * D + c)[chunk] =
+              v;
+        else
+          reinterpret_cast<uint4*>(a.ws_acc + ((row_base + to) * a.max_shards + shard) * D +
+                                   c)[chunk] = v;
+      }
+      __syncwarp();
     }
     tc_fence_before();
   }
@@ -686,10 +759,11 @@ __global__ void __launch_bounds__(kChunkCombineRows * 32)
   const int h = (blockIdx.x / blocks) % a.Hkv;
   const int slot = blockIdx.x / (blocks * a.Hkv);
   const int r = (blockIdx.x % blocks) * kChunkCombineRows + warp;
-  grid_dependency_wait();
-  grid_launch_dependents();
+  // (the lengths and offsets were complete before the attention kernel began)
   const ChunkItem it = chunk_item<KT>(a, slot, lane);
   const int tok = r / a.G, g = r % a.G;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (!it.any || it.shards < 2 || r >= rows || it.t0 + tok >= it.t1) return;
   const size_t row = (size_t)(it.row0 + tok) * a.Hq + (size_t)h * a.G + g;
   if (!PGD_IN(row, (size_t)a.total * a.Hq, a.err)) return;
@@ -709,7 +783,7 @@ __global__ void __launch_bounds__(kChunkCombineRows * 32)
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
   if (!dead && M != -INFINITY) {
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < it.shards; ++s) {
       const float2 v = __ldcg(ml + s);
       const float c = fast_exp2(v.x - M);
