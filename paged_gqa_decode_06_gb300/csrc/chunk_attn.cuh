@@ -34,8 +34,9 @@
 // zero would carry it to the others.
 //
 // P is rounded once to the element type for the second product (the weights
-// of a row are at most 2^8 and the largest is at least 1, so each keeps that
-// type's relative precision); sums, maxima and accumulators are fp32.
+// of a row are at most 2^15, in bf16 2^60, and the largest is at least 1, so
+// each keeps that type's relative precision); sums, maxima and accumulators are
+// fp32.
 #pragma once
 
 #include <type_traits>
@@ -97,6 +98,7 @@ template <int kRing, int kStreams, int kKeys, int kMaxEdges>
 struct ChunkShared {
   ChunkBars<kRing, kStreams, kKeys / 64> bar;
   ChunkItem item;
+  __align__(16) int32_t coord[16];  // row groups of a tile's pieces
   uint32_t tmem;
   int32_t abort;
   int32_t bad_lo, bad_hi;  // positions in pages outside the pool
@@ -278,20 +280,20 @@ __device__ __forceinline__ void chunk_issue(typename ChunkCfg<D>::Bars& bar, uin
     issue_s(0, 1);
   int cleaned = 0;        // edge tiles looked over so far
   bool told = false;      // V of this tile has landed and, an edge tile's, been handed over
+  bool is_edge = edge(0);
   for (int j = 0; j < ntiles && ok; ++j) {
-    const bool is_edge = edge(j);
     if (!told) {
       wait(&bar.full[vp.slot], vp.phase);
       if (is_edge) mbar_arrive(smem_u32(&bar.v_edge));
     }
-    told = false;
+    const bool look = is_edge;
 #pragma unroll
     for (int s = 0; s < NA; ++s) {
       const int buf = NA == 2 ? s : (j & 1), phase = NA == 2 ? (j & 1) : ((j >> 1) & 1);
 #pragma unroll
       for (int part = 0; part < C::kParts; ++part) {
         wait(&bar.p_full[buf][part], phase);
-        if (part == 0 && s == 0 && is_edge) wait(&bar.v_clean, cleaned++ & 1);
+        if (part == 0 && s == 0 && look) wait(&bar.v_clean, cleaned++ & 1);
         if (!ok) return;
         tc_fence_after();
         const uint64_t v0 = vd + vp.slot * kTile16 + part * (64 * D * 2 / 16);
@@ -306,15 +308,14 @@ __device__ __forceinline__ void chunk_issue(typename ChunkCfg<D>::Bars& bar, uin
       if (s == NA - 1) {
         tc_commit(smem_u32(&bar.empty[vp.slot]));
         vp.next();
+        // What the next tile needs is seen to here, where the products queued
+        // above still run: V, if it has come already, and an edge tile's is
+        // handed over to be looked at while the weights are made.
+        is_edge = edge(j + 1);
+        told = j + 1 < ntiles && mbar_try_wait(smem_u32(&bar.full[vp.slot]), vp.phase);
+        if (told && is_edge) mbar_arrive(smem_u32(&bar.v_edge));
       }
       if (j + (NA == 2 ? 1 : 2) < ntiles) issue_s(s, buf);
-    }
-    // an edge tile whose V has come already is handed over now, and looked
-    // over while its weights are made
-    if (j + 1 < ntiles && edge(j + 1) &&
-        mbar_try_wait(smem_u32(&bar.full[vp.slot]), vp.phase)) {
-      mbar_arrive(smem_u32(&bar.v_edge));
-      told = true;
     }
   }
 }
@@ -410,12 +411,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const int ntiles = (int)((int64_t)it.tiles * (shard + 1) / it.shards) - tile0;
   const int key0 = it.base + tile0 * KT;  // first key of this CTA's first tile
   const int ns = (it.t1 - it.t0) > a.tile_tok ? NS : 1;  // streams with tokens
-  // whether some row of the CTA does not attend all of tile j
-  const int plast = it.p0 + (it.t1 - it.t0) - 1;
-  auto edge = [&](int j) {
-    const int k0 = key0 + j * KT;
-    return k0 + KT - 1 > it.p0 || (a.window > 0 && k0 <= plast - a.window);
-  };
+  // whether some row of the CTA does not attend all of tile j: its last key
+  // is after the first row's position, or its first before the last's window
+  const int edge_from = max(0, it.p0 - key0 + 1) / KT;
+  const int edge_to =
+      a.window > 0 ? it.p0 + (it.t1 - it.t0) - 1 - a.window - key0 : -1;
+  auto edge = [&](int j) { return j >= edge_from || j * KT <= edge_to; };
 
   // two streams: 384 threads launched with 168 registers each; the row threads
   // (128 scores apiece) take 200, the last warpgroup 104
@@ -433,18 +434,23 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       __syncwarp();
       const int pieces = KT / a.box_t;
       const int pool_groups = a.num_pages * (a.page_size / 8);
+      // The page of this lane's piece of tile j, read a tile ahead (clamped to
+      // the table: the address is always good, and nothing waits for it here).
+      auto page_of = [&](int j) {
+        const int page = (key0 + j * KT + lane * a.box_t) >> a.page_shift;
+        const size_t pi = (size_t)it.b * a.max_pages + min(page, a.max_pages - 1);
+        return PGD_IN(pi, (size_t)a.B * a.max_pages, a.err) ? ld_global_s32(a.page_table + pi) : -1;
+      };
       int issued = 0;
-      int coord = 0;
+      int phys = page_of(0);
       for (int r = 0; r < 2 * ntiles; ++r) {
         const int slot_r = r % NR;
-        if ((r & 1) == 0 && lane < pieces) {
-          // this lane's piece of the tile: a row group of the pool, or one past
-          // it (zeros) where no query attends
+        if ((r & 1) == 0) {
+          // where the pieces of the tile are: a row group of the pool, or one
+          // past it (zeros) where no query attends
           const int ptok = key0 + (r >> 1) * KT + lane * a.box_t;
-          coord = pool_groups;
-          if (ptok < it.hi && ptok + a.box_t > it.lo) {
-            const size_t pi = (size_t)it.b * a.max_pages + (ptok >> a.page_shift);
-            const int phys = PGD_IN(pi, (size_t)a.B * a.max_pages, a.err) ? a.page_table[pi] : -1;
+          int coord = pool_groups;
+          if (lane < pieces && ptok < it.hi && ptok + a.box_t > it.lo) {
             if (phys < 0 || phys >= a.num_pages) {
               raise_error(a.err, DECODE_ATTN_DEV_BAD_PAGE);
               atomicMin(&sh.bad_lo, ptok);
@@ -453,8 +459,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
               coord = (phys << (a.page_shift - 3)) + ((ptok & (a.page_size - 1)) >> 3);
             }
           }
+          __syncwarp();
+          if (lane < 16) sh.coord[lane] = coord;
+          phys = page_of((r >> 1) + 1);
         }
-        __syncwarp();
         if (r >= NR) {
           int go = 1;
           if (lane == 0) {
@@ -466,12 +474,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) break;
         }
-        const uint32_t fb = smem_u32(&bar.full[slot_r]);
-        if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes + (r == 0 ? a.stall_tx : 0));
         __syncwarp();
-        if (lane < pieces)
-          tma_load_5d(smem_u32(ring + slot_r * C::kTileBytes + lane * a.box_t * D * 2),
-                      (r & 1) ? &tmap_v : &tmap_k, 0, 0, 0, coord, h, fb);
+        if (elect_one()) {
+          // one lane issues every box: lanes in turn cost four times as much
+          const uint32_t fb = smem_u32(&bar.full[slot_r]);
+          mbar_arrive_expect_tx(fb, C::kTileBytes + (r == 0 ? a.stall_tx : 0));
+          const CUtensorMap* map = (r & 1) ? &tmap_v : &tmap_k;
+          uint32_t dst = smem_u32(ring + slot_r * C::kTileBytes);
+          const uint32_t step = a.box_t * D * 2;
+          for (int p = 0; p < pieces; p += 4) {
+            const int4 c = *reinterpret_cast<const int4*>(&sh.coord[p]);
+            tma_load_5d(dst, map, 0, 0, 0, c.x, h, fb);
+            if (pieces > 1) tma_load_5d(dst + step, map, 0, 0, 0, c.y, h, fb);
+            if (pieces > 2) {
+              tma_load_5d(dst + 2 * step, map, 0, 0, 0, c.z, h, fb);
+              tma_load_5d(dst + 3 * step, map, 0, 0, 0, c.w, h, fb);
+            }
+            dst += 4 * step;
+          }
+        }
+        __syncwarp();
         issued = r + 1;
       }
       // this CTA's copies in flight have landed before the warp exits
@@ -558,6 +580,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY;
     uint64_t l2 = 0;  // two partial sums
+    constexpr float kGrow = std::is_same<E, __nv_bfloat16>::value ? 60.f : 15.f;
     bool ok = true;
     auto wait = [&](uint64_t* b, int parity) {
       if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
@@ -593,52 +616,66 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         }
         mult = 1.f;
       }
-      float top[4] = {x[0], x[1], x[2], x[3]};
+      auto row_max = [&] {
+        float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int i = 4; i < KT; i += 4) {
-        top[(i >> 2) & 1] = max3(top[(i >> 2) & 1], x[i], x[i + 1]);
-        top[2 + ((i >> 2) & 1)] = max3(top[2 + ((i >> 2) & 1)], x[i + 2], x[i + 3]);
-      }
-      const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * mult;
-      // The reference maximum follows only when it would grow by more than
-      // 2^8: the weights stay below that, and the accumulator is rescaled
-      // for a few tiles instead of nearly every one.
-      const bool grow = mx > m + 8.f;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float alpha = grow ? fast_exp2(m - mx) : 1.f;
-        if (grow) m = mx;
-        if (j > 0) {
-          // O holds the products up to the unit before: rescale it in place
-          wait(&bar.o_full[s], (j - 1) & 1);
-          __syncwarp();
-          tc_fence_after();
-          l2 = mul2(l2, pair(alpha, alpha));
-#pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            const uint32_t at = tmem_o + s * D + lanes + c;
-            tmem_ld16(o, at);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= alpha;
-            tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
-          }
+        for (int i = 4; i < KT; i += 4) {
+          top[(i >> 2) & 1] = max3(top[(i >> 2) & 1], x[i], x[i + 1]);
+          top[2 + ((i >> 2) & 1)] = max3(top[2 + ((i >> 2) & 1)], x[i + 2], x[i + 3]);
         }
-      }
-      const float mu = m == -INFINITY ? 0.f : m;  // a row without a key so far
-      const uint64_t mult2 = pair(mult, mult), nm2 = pair(-mu, -mu);
-#pragma unroll
-      for (int part = 0; part < C::kParts; ++part) {
-        uint32_t w[32];
+        return fmaxf(max3(top[0], top[1], top[2]), top[3]) * mult;
+      };
+      // 64 keys' weights against the reference maximum, and their sum
+      uint32_t w[32];
+      auto weigh = [&](int part) {
+        const float mu = m == -INFINITY ? 0.f : m;  // a row without a key so far
+        const uint64_t mult2 = pair(mult, mult), nm2 = pair(-mu, -mu);
+        uint64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int k = part * 64 + 2 * i;
           const float2 e = unpair(fma2(pair(x[k], x[k + 1]), mult2, nm2));
           const float p0 = fast_exp2(e.x), p1 = fast_exp2(e.y);
-          l2 = add2(l2, pair(p0, p1));
+          sum = add2(sum, pair(p0, p1));
           w[i] = ElemOps<E>::pack2(p0, p1);
         }
+        return sum;
+      };
+      // The reference maximum follows only when the weights would grow beyond
+      // kGrow powers of two (which both formats and the 32-bit sums hold, and
+      // every value keeps its relative precision): the accumulator is seldom
+      // rescaled.  So the first weights are made against it while the tile's
+      // maximum is still being taken, and made again in the tiles that move it.
+      if (j == 0) m = row_max();
+      uint64_t sum = weigh(0);
+      const float mx = row_max();
+      const bool grow = mx > m + kGrow;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = grow ? fast_exp2(m - mx) : 1.f;
+        if (grow) m = mx;
+        // O holds the products up to the unit before: rescale it in place
+        // (not reached in the first tile, whose maximum is the reference)
+        wait(&bar.o_full[s], (j - 1) & 1);
+        __syncwarp();
+        tc_fence_after();
+        l2 = mul2(l2, pair(alpha, alpha));
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          const uint32_t at = tmem_o + s * D + lanes + c;
+          tmem_ld16(o, at);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] *= alpha;
+          tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
+        }
+        sum = weigh(0);
+      }
+#pragma unroll
+      for (int part = 0; part < C::kParts; ++part) {
+        if (part > 0) sum = weigh(part);
         tmem_st32(tm_s + part * 32, w);
+        l2 = add2(l2, sum);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
