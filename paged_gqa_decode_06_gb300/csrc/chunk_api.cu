@@ -60,6 +60,11 @@ int run_chunk(const decode_attn_params* p, const decode_attn_chunk_plan& plan, i
   a.slots = plan.slots;
   a.max_shards = plan.max_shards;
   a.shard_tiles = plan.shard_keys / tile_keys(D);
+  a.by_item = FastDiv::of(a.item_tok);
+  a.by_heads = FastDiv::of(a.Hkv);
+  a.by_shards = FastDiv::of(a.max_shards);
+  a.by_shard_tiles = FastDiv::of(a.shard_tiles);
+  a.by_group = FastDiv::of(G);
   a.stall_tx = env_positive("DECODE_ATTN_TEST_STALL_TX");  // a test's hook; unset in normal use
   a.scale_log2 = p->scale * kLog2e;
   if (plan.max_shards > 1) {

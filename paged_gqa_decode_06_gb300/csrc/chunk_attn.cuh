@@ -64,6 +64,7 @@ struct ChunkArgs {
   int32_t item_tok;           // tokens of one CTA (all streams)
   int32_t slots;              // tiles of item_tok tokens over all sequences, at most
   int32_t max_shards, shard_tiles;
+  FastDiv by_item, by_heads, by_shards, by_shard_tiles, by_group;
   int32_t stall_tx;           // 0; a test sets extra bytes on the first K tile's barrier
   float scale_log2;
 };
@@ -139,7 +140,8 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, in
   if (a.B < 32) {  // one round trip: every offset and length at once
     const int32_t off = lane <= a.B ? ld_global_s32(a.offsets + lane) : 0;
     const int32_t len = lane < a.B ? ld_global_s32(a.seq_lens + lane) : 0;
-    b = __popc(__ballot_sync(0xffffffffu, lane < a.B && off / a.item_tok + lane <= slot)) - 1;
+    const bool le = lane < a.B && (int)a.by_item.div(max(off, 0)) + lane <= slot;
+    b = __popc(__ballot_sync(0xffffffffu, le)) - 1;
     if (b < 0) return it;
     const int32_t z = __shfl_sync(0xffffffffu, off, b + 1);
     r.first = __shfl_sync(0xffffffffu, off, b);
@@ -148,7 +150,7 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, in
     L = __shfl_sync(0xffffffffu, len, b);
   } else {
     b = warp_search(a.B, slot, lane,
-                    [&](int i) { return (int64_t)(a.offsets[i] / a.item_tok) + i; });
+                    [&](int i) { return (int64_t)a.by_item.div(max(a.offsets[i], 0)) + i; });
     if (b < 0) return it;
     r = row_range(a.offsets, b, a.total);
     L = ld_global_s32(a.seq_lens + b);
@@ -158,7 +160,7 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, in
     it.status = DECODE_ATTN_DEV_BAD_LEN;
     return it;
   }
-  const int64_t t0 = ((int64_t)slot - (r.first / a.item_tok + b)) * a.item_tok;
+  const int64_t t0 = ((int64_t)slot - (a.by_item.div(r.first) + b)) * a.item_tok;
   if (t0 < 0 || t0 >= r.count) return it;
   it.any = true;
   it.t0 = (int32_t)t0;
@@ -173,7 +175,7 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int slot, in
   it.lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
   it.base = it.lo & ~(KT - 1);
   it.tiles = it.hi > it.lo ? (it.hi - it.base + KT - 1) / KT : 0;
-  it.shards = min(a.max_shards, (it.tiles + a.shard_tiles - 1) / a.shard_tiles);
+  it.shards = min(a.max_shards, (int)a.by_shard_tiles.div(it.tiles + a.shard_tiles - 1));
   return it;
 }
 
@@ -366,10 +368,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const int h = blockIdx.x % a.Hkv;
-  const int shard = (blockIdx.x / a.Hkv) % a.max_shards;
+  const int rest = a.by_heads.div(blockIdx.x), h = blockIdx.x - rest * a.Hkv;
+  const int place = a.by_shards.div(rest), shard = rest - place * a.max_shards;
   // the last tiles of a sequence see the most keys: they start first
-  const int slot = a.slots - 1 - blockIdx.x / (a.Hkv * a.max_shards);
+  const int slot = a.slots - 1 - place;
   // The issuing warp allocates the tensor memory while the others look for
   // their item, and takes it from them.
   constexpr int kOthers = NS * 128 + 32;  // the row threads and the issuing warp
@@ -407,8 +409,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     return;
   }
   if (shard >= it.shards) return;
-  const int tile0 = (int)((int64_t)it.tiles * shard / it.shards);
-  const int ntiles = (int)((int64_t)it.tiles * (shard + 1) / it.shards) - tile0;
+  // (at most 2^24 tiles and 128 shards)
+  int tile0 = 0, ntiles = it.tiles;
+  if (it.shards > 1) {
+    tile0 = (uint32_t)it.tiles * shard / (uint32_t)it.shards;
+    ntiles = (uint32_t)it.tiles * (shard + 1) / (uint32_t)it.shards - tile0;
+  }
   const int key0 = it.base + tile0 * KT;  // first key of this CTA's first tile
   const int ns = (it.t1 - it.t0) > a.tile_tok ? NS : 1;  // streams with tokens
   // whether some row of the CTA does not attend all of tile j: its last key
@@ -423,15 +429,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   if (warp >= kProducer) {
     if constexpr (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kProducer) {
-      if (lane == 0) {
-        const uint32_t qb = smem_u32(&bar.q_full);
-        mbar_arrive_expect_tx(qb, (uint32_t)(ns * (D / 64) * a.tile_tok * a.G * 128));
-        for (int s = 0; s < ns; ++s)
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(smem_u32(smem + s * C::kQBytes + c * (128 * 128)), &tmap_q, 0, h * a.G,
-                        it.row0 + s * a.tile_tok, c, qb);
-      }
-      __syncwarp();
       const int pieces = KT / a.box_t;
       const int pool_groups = a.num_pages * (a.page_size / 8);
       // The page of this lane's piece of tile j, read a tile ahead (clamped to
@@ -441,8 +438,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         const size_t pi = (size_t)it.b * a.max_pages + min(page, a.max_pages - 1);
         return PGD_IN(pi, (size_t)a.B * a.max_pages, a.err) ? ld_global_s32(a.page_table + pi) : -1;
       };
-      int issued = 0;
       int phys = page_of(0);
+      if (elect_one()) {
+        const uint32_t qb = smem_u32(&bar.q_full);
+        mbar_arrive_expect_tx(qb, (uint32_t)(ns * (D / 64) * a.tile_tok * a.G * 128));
+        for (int s = 0; s < ns; ++s)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem_u32(smem + s * C::kQBytes + c * (128 * 128)), &tmap_q, 0, h * a.G,
+                        it.row0 + s * a.tile_tok, c, qb);
+      }
+      __syncwarp();
+      int issued = 0;
       for (int r = 0; r < 2 * ntiles; ++r) {
         const int slot_r = r % NR;
         if ((r & 1) == 0) {
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   if (s < ns) {
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int tok = row / a.G;
+    const int tok = a.by_group.div(row);
     const int te = min(it.t1, it.t0 + (s + 1) * a.tile_tok);  // one past the stream's tokens
     const int first_pos = it.p0 + s * a.tile_tok, last_pos = it.p0 + (te - it.t0) - 1;
     const int pos = first_pos + tok;  // this row's position
@@ -692,7 +698,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         !ok || (pos >= sh.bad_lo && (a.window <= 0 || pos - a.window + 1 < sh.bad_hi));
     // this row among the CTA's output rows, or -1
     const size_t row_base = (size_t)it.row0 * a.Hq + (size_t)h * a.G;
-    int rel = (s * a.tile_tok + tok) * a.Hq + row % a.G;
+    int rel = (s * a.tile_tok + tok) * a.Hq + row - tok * a.G;
     if (tok >= a.tile_tok || it.t0 + s * a.tile_tok + tok >= te ||
         !PGD_IN(row_base + rel, (size_t)a.total * a.Hq, a.err))
       rel = -1;
@@ -728,30 +734,33 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     if (!whole && rel >= 0)
       a.ws_ml[(row_base + rel) * a.max_shards + shard] = make_float2(m, dead ? -1.f : l);
     uint4* stage = reinterpret_cast<uint4*>(smem + s * C::kQBytes) + (warp & 3) * 256;
-    const int step = whole ? 64 : 32;  // columns of 128 bytes
-    for (int c = 0; c < D; c += step) {
+    // bytes of 32 columns of a row: 64 of the output, 128 of a partial
+    uint8_t* dst = whole ? static_cast<uint8_t*>(a.out) + row_base * D * 2
+                         : reinterpret_cast<uint8_t*>(
+                               a.ws_acc + (row_base * a.max_shards + shard) * D);
+    const int row_bytes = whole ? D * 2 : a.max_shards * D * 4;
+    const int per_row = whole ? 4 : 8;  // lanes of 16 bytes
+    const int chunk = lane & (per_row - 1), first = whole ? lane >> 2 : lane >> 3;
+    // (a small loop: a CTA runs it once, and most of its time would be the
+    // fetching of unrolled code)
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tmem_ld32(o, tmem_o + s * D + lanes + c);
+      tmem_wait_ld();
+      if (sh.wild_any && rel >= 0) patch(c, o);
       if (whole) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float o[32];
-          tmem_ld32(o, tmem_o + s * D + lanes + c + 32 * k);
-          tmem_wait_ld();
-          if (sh.wild_any && rel >= 0) patch(c + 32 * k, o);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            stage[lane * 8 + ((4 * k + i) ^ (lane & 7))] =
-                make_uint4(ElemOps<E>::pack2(o[8 * i], o[8 * i + 1]),
-                           ElemOps<E>::pack2(o[8 * i + 2], o[8 * i + 3]),
-                           ElemOps<E>::pack2(o[8 * i + 4], o[8 * i + 5]),
-                           ElemOps<E>::pack2(o[8 * i + 6], o[8 * i + 7]));
+          for (int k = 0; k < 4; ++k) {
+            const float x = o[8 * i + 2 * k] * inv, y = o[8 * i + 2 * k + 1] * inv;
+            w[k] = inv == 0.f ? 0u : ElemOps<E>::pack2(x, y);
+          }
+          stage[lane * 8 + (i ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       } else {
-        float o[32];
-        tmem_ld32(o, tmem_o + s * D + lanes + c);
-        tmem_wait_ld();
-        if (sh.wild_any && rel >= 0) patch(c, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           stage[lane * 8 + (i ^ (lane & 7))] =
@@ -759,19 +768,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
                          __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
       }
       __syncwarp();
-      const int chunk = lane & 7;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
+      uint8_t* at = dst + (whole ? c * 2 : c * 4) + chunk * 16;
+#pragma unroll 4
+      for (int r = first; r < 32; r += 32 / per_row) {
         const uint4 v = stage[r * 8 + (chunk ^ (r & 7))];
         const int to = __shfl_sync(0xffffffffu, rel, r);
-        if (to < 0) continue;
-        if (whole)
-          reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (row_base + to) * D + c)[chunk] =
-              v;
-        else
-          reinterpret_cast<uint4*>(a.ws_acc + ((row_base + to) * a.max_shards + shard) * D +
-                                   c)[chunk] = v;
+        if (to >= 0) *reinterpret_cast<uint4*>(at + (size_t)to * row_bytes) = v;
       }
       __syncwarp();
     }
