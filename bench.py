@@ -22,7 +22,6 @@ from __future__ import annotations
 import argparse
 import datetime
 import hashlib
-import glob
 import json
 import os
 import platform
@@ -211,9 +210,16 @@ class ClockSampler:
 
 # ------------------------------------------------------------ traffic record
 
+# sources of the kernels that a decode step launches (and of their launchers)
+DECODE_SOURCES = ("api.cu", "combine.cuh", "device_common.cuh", "elem.cuh", "kernels_d128.cu",
+                  "kernels_d256.cu", "kernels_d64.cu", "kernels_dim.inc", "kv_append.cu",
+                  "launch.h", "split_mma.cuh", "split_simt.cuh", "static_scratch.cu")
+
+
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "paged_gqa_decode_06_gb300", "csrc", "*"))):
+    for name in DECODE_SOURCES:
+        f = os.path.join(ROOT, "paged_gqa_decode_06_gb300", "csrc", name)
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())
             h.update(fh.read())
