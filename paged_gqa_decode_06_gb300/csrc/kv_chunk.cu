@@ -10,12 +10,16 @@
 // 8 threads of a head are neighbours in a warp and the row's maximum is a few
 // shuffles.
 //
-// Memory bounds them, and what reaches its rate is the number of loads in
+// Memory bounds the read, and what reaches its rate is the number of loads in
 // flight: all loads of kBatch items before the first store.  131072 rows of 8
 // heads of 128 read from e4m3: 124 us, 6.5 TB/s (with 1 item 151, with 4
 // items, and fewer blocks per SM for their registers, 127; 4 rows per block
-// 160, 16 rows 128).  32,400 fp16 rows appended as e4m3: 40 us (50, 43, 48, 43),
-// of which about 5 are the launch and the first rows' placing.
+// 160, 16 rows 128).  A quantising append issues as much as it moves (80 % of
+// the issue slots with each tensor's maximum shuffled by itself): K's and V's
+// row maxima share one shuffle as the halves of a word, and the count of
+// shuffles is fixed at compile time.  32,354 fp16 rows: 36.6 us, 5.5 TB/s
+// (with separate shuffles in a loop 40.5), of which about 5 are the launch and
+// the placing of the first rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -78,27 +82,28 @@ __device__ __forceinline__ void check_offsets(const KvRows& a) {
     if (!row_range(a.offsets, b, a.total).ok) raise_error(a.err, DECODE_ATTN_DEV_BAD_LEN);
 }
 
-// Larger magnitudes of two pairs of 16-bit values; a NaN only if both are.
+// Of two pairs of 16-bit values the larger magnitudes, with any sign; a NaN
+// only where both are.
 template <class E>
 __device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
-  if constexpr (std::is_same<E, __nv_bfloat16>::value) {
-    const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<__nv_bfloat162*>(&a)),
-                                     __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
-    return *reinterpret_cast<const uint32_t*>(&m);
-  } else {
-    const __half2 m =
-        __hmax2(__habs2(*reinterpret_cast<__half2*>(&a)), __habs2(*reinterpret_cast<__half2*>(&b)));
-    return *reinterpret_cast<const uint32_t*>(&m);
-  }
+  uint32_t r;
+  if constexpr (std::is_same<E, __nv_bfloat16>::value)
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-template <class E, bool kQuant>
+// kLanes threads hold a head's row (D / 8); 0: 16-bit rows, copied.
+template <class E, int kLanes>
 __global__ void __launch_bounds__(kThreads) kv_append_rows_kernel(const KvRows a) {
-  __shared__ int2 place_s[kMaxRows];
+  constexpr bool kQuant = kLanes > 0;
+  __shared__ int64_t cell_s[kMaxRows];   // a row's first 8 values in the pool, or -1
+  __shared__ int64_t scale_s[kMaxRows];  // its first head's scale
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * a.rows_per_block;
   const int rows = min(a.rows_per_block, a.total - row0);
-  const int per_head = 1 << a.head_shift, per_row = a.Hkv << a.head_shift, items = rows * per_row;
+  const int per_row = a.Hkv << a.head_shift, items = rows * per_row;
   const size_t cells = (size_t)a.num_pages * a.page_size * per_row;
   const uint4* src[2] = {static_cast<const uint4*>(a.src[0]) + (size_t)row0 * per_row,
                          static_cast<const uint4*>(a.src[1]) + (size_t)row0 * per_row};
@@ -118,7 +123,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_rows_kernel(const KvRows a
   if (warp < rows) {
     bool owned;
     const int2 at = place_row<true>(a, row0 + warp, lane, &owned);
-    if (lane == 0) place_s[warp] = at;
+    if (lane == 0) {
+      cell_s[warp] = at.x < 0 ? -1 : ((int64_t)at.x * a.page_size + at.y) * per_row;
+      scale_s[warp] = (int64_t)at.x * a.Hkv * a.page_size + at.y;
+    }
   }
   check_offsets(a);
   __syncthreads();
@@ -131,22 +139,29 @@ __global__ void __launch_bounds__(kThreads) kv_append_rows_kernel(const KvRows a
       if (e - lane >= items) break;
       const int r = e < items ? (int)a.by_row.div(e) : 0;
       const int c = e < items ? e - r * per_row : 0;
-      const int2 at = place_s[r];
-      const size_t cell = ((size_t)at.x * a.page_size + at.y) * per_row + c;
-      const bool go = e < items && at.x >= 0 && PGD_IN(cell, cells, a.err);
+      const int64_t first = cell_s[r];
+      const size_t cell = first + c;
+      const bool go = e < items && first >= 0 && PGD_IN(cell, cells, a.err);
       if constexpr (!kQuant) {
         if (go)
           for (int i = 0; i < 2; ++i) static_cast<uint4*>(a.dst[i])[cell] = x[u][i];
       } else {
+        // the largest magnitudes of K's values (low half) and V's
+        uint32_t top[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          top[i] = top2<E>(top2<E>(x[u][i].x, x[u][i].y), top2<E>(x[u][i].z, x[u][i].w));
+        uint32_t both = top2<E>(__byte_perm(top[0], top[1], 0x5410),
+                                __byte_perm(top[0], top[1], 0x7632));
+#pragma unroll
+        for (int k = 1; k < kLanes; k <<= 1)
+          both = top2<E>(both, __shfl_xor_sync(0xffffffffu, both, k));
+        const float2 amax = ElemOps<E>::unpack2(both & 0x7fff7fffu);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 v = x[u][i];
-          uint32_t top = top2<E>(top2<E>(v.x, v.y), top2<E>(v.z, v.w));
-          for (int k = 1; k < per_head; k <<= 1)
-            top = top2<E>(top, __shfl_xor_sync(0xffffffffu, top, k));
-          const float2 t = ElemOps<E>::unpack2(top);
-          const RowScale s = e4m3_scale(fmaxf(0.f, fmaxf(t.x, t.y)));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          // (a row of NaN alone counts as zeros)
+          const RowScale s = e4m3_scale(fmaxf(0.f, i ? amax.y : amax.x));
+          const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
           uint32_t q[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -155,10 +170,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_rows_kernel(const KvRows a
           }
           if (!go) continue;
           static_cast<uint2*>(a.dst[i])[cell] =
-              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-          if ((c & (per_head - 1)) == 0)
-            a.scales[i][((size_t)at.x * a.Hkv + (c >> a.head_shift)) * a.page_size + at.y] =
-                s.scale;
+              make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+          if ((c & (kLanes - 1)) == 0)
+            a.scales[i][scale_s[r] + (c >> a.head_shift) * a.page_size] = s.scale;
         }
       }
     }
@@ -301,10 +315,19 @@ extern "C" int decode_kv_append_chunk(const decode_attn_params* p, int32_t kv_fo
   a.base = seq_lens;
   a.err = err_flag;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!quant) return launch_rows(kv_append_rows_kernel<__half, false>, a, s);  // a copy
-  return p->dtype == DECODE_ATTN_DTYPE_BF16
-             ? launch_rows(kv_append_rows_kernel<__nv_bfloat16, true>, a, s)
-             : launch_rows(kv_append_rows_kernel<__half, true>, a, s);
+  if (!quant) return launch_rows(kv_append_rows_kernel<__half, 0>, a, s);  // a copy
+  const bool bf16 = p->dtype == DECODE_ATTN_DTYPE_BF16;
+  switch (a.D) {
+    case 64:
+      return bf16 ? launch_rows(kv_append_rows_kernel<__nv_bfloat16, 8>, a, s)
+                  : launch_rows(kv_append_rows_kernel<__half, 8>, a, s);
+    case 128:
+      return bf16 ? launch_rows(kv_append_rows_kernel<__nv_bfloat16, 16>, a, s)
+                  : launch_rows(kv_append_rows_kernel<__half, 16>, a, s);
+    default:
+      return bf16 ? launch_rows(kv_append_rows_kernel<__nv_bfloat16, 32>, a, s)
+                  : launch_rows(kv_append_rows_kernel<__half, 32>, a, s);
+  }
 }
 
 extern "C" int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total_rows,
