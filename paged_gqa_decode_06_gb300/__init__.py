@@ -516,7 +516,7 @@ def _cuda_index(t, name: str, call: str) -> int:
 def _raw_stream(stream, index: int) -> int:
     """_stream_handle for tensors on the current device `index`."""
     if stream is None:
-            return torch._C._cuda_getCurrentRawStream(index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return _stream_handle(stream)
 
 
@@ -740,14 +740,15 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
     if fmt == KV_16BIT and dtype != k_pages.dtype:
         raise TypeError(f"16-bit pools are read back as they are ({k_pages.dtype})")
     shape = (int(total_rows), *k_pages.shape[2:])
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _need(t, dtype, name, index)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _need(t, dtype, name, index)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
+        v_out = torch.empty_like(k_out)
     p = _params(B, k_pages.shape[2], k_pages.shape, page_table.shape[1], 0, 1.0, 0, dtype)
     st = load_library().decode_kv_read(
         ctypes.byref(p), fmt, shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
