@@ -136,12 +136,17 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
                               : D == 128 ? QuantCfg<128>::kStages : QuantCfg<256>::kStages;
   // the merge, by the 16-bit planner's rule: a cluster for one-wave plans of
   // 2..8 shards (16 on grids of at most 64 CTAs) that fill 4/5 of the slots
-  // or are small
+  // or are small, where the receive buffer leaves room for the CTAs of an SM
+  // (16 rows of head_dim 128 do not: 8 sequences of 65536, pages of 16, 346 us
+  // by clusters, one CTA per SM, and 195 us through the workspace)
+  const int recv = ClusterRecv::of(T * G * HC, D, (int)std::min<int64_t>(shards, 16)).bytes;
   const bool cluster_ok =
       plan->split && one_wave_grid && (shards <= 8 || (shards <= 16 && ctas <= 64));
   if (p->schedule == DECODE_ATTN_SCHEDULE_CLUSTER && !cluster_ok) return DECODE_ATTN_ERR_VARIANT;
   if (p->schedule == DECODE_ATTN_SCHEDULE_CLUSTER ||
       (p->schedule == DECODE_ATTN_SCHEDULE_AUTO && cluster_ok &&
+       recv <= (D == 64 ? QuantCfg<64>::kRecvRoom
+                        : D == 128 ? QuantCfg<128>::kRecvRoom : QuantCfg<256>::kRecvRoom) &&
        (ctas * 5 >= slots * 4 || (double)units * span * row_bytes <= (double)(32 << 20))))
     plan->cluster = (int32_t)shards;
   if (plan->split) {

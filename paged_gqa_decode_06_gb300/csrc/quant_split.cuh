@@ -3,11 +3,11 @@
 // scores scale * ks_t * (q . kc_t).
 //
 // The shape of the 16-bit split kernel (split_mma.cuh): one CTA per (shard,
-// KV head, sequence), a producer warp filling a shared-memory ring by TMA,
-// four consumer warps of 16 positions each, mma.sync with the tokens on M and
-// the group's query rows on N, and the same merges (workspace, or a cluster's
-// distributed shared memory).  What differs is what a stage holds and how the
-// fragments come out of it:
+// KV head or two, sequence), one or two producer warps filling a shared-memory
+// ring by TMA, pairs of consumer warps that take its stages in turn, mma.sync
+// with the tokens on M and the group's query rows on N, and the same merges
+// (workspace, or a cluster's distributed shared memory).  What differs is what
+// a stage holds and how the fragments come out of it:
 //  * A stage is 64 positions of codes (half the bytes), so twice the stages
 //    are in flight; the scales of its positions follow by cp.async, 16 bytes
 //    (4 positions of one head; they lie [P][Hkv][PS]) per lane.
@@ -37,9 +37,9 @@ namespace pgd {
 // a page's piece is too small for the copy engine: a box costs about 45 ns
 // whatever it brings, and a box can hold the rows of several heads (GB300,
 // pages of 16: 64 sequences of U[1, 8192] positions 125 -> 114 us, a thousand
-// of U[1, 512] 193 -> 140 us, head_dim 256 118 -> 108 us).  A stage
-// then holds half the positions, and the two warps that share it take a head
-// each.  Everything after the streams sees one KV head with twice the query
+// of U[1, 512] 193 -> 140 us, head_dim 256 118 -> 108 us).  A stage then
+// holds half the positions, and the two warps that share it take a head each.
+// Everything after the streams sees one KV head with twice the query
 // heads.
 struct QuantArgs {
   SplitArgs s;            // as for the 16-bit split kernel; G and Hkv of HC heads as one
@@ -48,7 +48,7 @@ struct QuantArgs {
   int32_t G1, heads;      // query heads per KV head, KV heads
 };
 
-template <int D, int NT8 = 1>
+template <int D, int NT8 = 1, int HC = 1>
 struct QuantCfg {
   // Consumer warps: pairs that share a stage, 32 positions a warp, the pairs
   // taking the stages in turn.  Turning codes into fragments is a long chain
@@ -56,7 +56,12 @@ struct QuantCfg {
   // positions, and there are as many pairs as the registers and the ring
   // (whose stages every pair must return to) allow.
   static constexpr int kWarps = NT8 == 2 && D <= 128 ? 4 : 6;
-  static constexpr int kThreads = (kWarps + 1) * 32;
+  // Warps that fill the ring.  The smaller stages of two heads' CTAs come twice
+  // as often, and two warps share them (64 sequences of U[1, 8192] positions
+  // 120 -> 115 us); with one head's the second only takes issue slots from the
+  // consumers (four sequences of 131072 201 -> 206 us).
+  static constexpr int kProducers = HC;
+  static constexpr int kThreads = (kWarps + kProducers) * 32;
   // CTAs of an SM: two, and one with twice the ring at D = 256, whose
   // accumulators and fragments need more registers than two leave.
   static constexpr int kCtas = D == 256 ? 1 : 2;
@@ -66,6 +71,10 @@ struct QuantCfg {
   static constexpr int kStages = (192 / kCtas) * 1024 / kStageBytes;  // 12, 6, 6
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kSmemBytes = kRingBytes + 1024;
+  // static shared memory (scales, row coordinates, warps' states), and what is
+  // left of a CTA's share of the SM's 228 KB for a cluster's receive buffer
+  static constexpr int kTableBytes = kStages * 2 * kTile * 4 + kMaxPieces * 4 + 1104;
+  static constexpr int kRecvRoom = 228 * 1024 / kCtas - 1024 - kSmemBytes - kTableBytes;
 };
 
 // Byte offset of (token t, 16-byte chunk c) of a CTA's head in a tile of codes
@@ -268,10 +277,10 @@ __device__ __forceinline__ float load_q_row(const uint16_t* row, bool live, int 
 
 // CL: a cluster plan, as in split_mma_body.
 template <int D, int NT8, class E, bool CL, int HC>
-__global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::kCtas)
+__global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT8, HC>::kCtas)
     quant_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const QuantArgs qa) {
-  using C = QuantCfg<D, NT8>;
+  using C = QuantCfg<D, NT8, HC>;
   constexpr int kPairs = C::kWarps / 2;
   static_assert(C::kStages % kPairs == 0, "a pair sees every phase of its stages");
   constexpr int KS = D / 16, kWarps = C::kWarps, GP = 8 * NT8;
@@ -289,6 +298,9 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::
   __shared__ int32_t bad_s;
   __shared__ volatile int32_t abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (written so that the code of one producer stays as it is without this)
+  const bool producer = C::kProducers == 1 ? warp == kWarps : warp >= kWarps;
+  const int part = C::kProducers == 1 ? 0 : warp - kWarps;
   uint8_t* ring = ring_base();
 
   if (threadIdx.x == kWarps * 32) {
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::
   // page ids of the first 32 pieces, read together with the length under the
   // guess that the sequence is as long as the plan's bound
   int spec_lo = -1, spec_phys = -1;
-  if (warp == kWarps) {
+  if (producer) {
     const SeqRange g =
         seq_range(a.len_hint, a.window, capacity, a.chunk, a.max_shards, a.T, a.balanced);
     if (g.status == 0 && s < g.nshards) {
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::
   const int n_tiles = (hi - shard_lo + kStagePos - 1) / kStagePos;
   const int pieces = kStagePos / box_t, n_pieces = n_tiles * pieces;
 
-  if (warp == kWarps) {
+  if (producer) {
     const int pool_rows = a.num_pages * a.page_size;  // past the pool: zeros
     int any_bad = 0;
 #pragma unroll 4
@@ -382,6 +394,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::
     if (__any_sync(0xffffffffu, any_bad)) {
       // no copy is issued; the consumers' first wait completes on plain
       // arrivals and they find the flag
+      if (part > 0) return;
       if (lane == 0) {
         bad_s = 1;
         raise_error(a.err, DECODE_ATTN_DEV_BAD_PAGE);
@@ -397,7 +410,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::
     const uint64_t policy = l2_evict_first_policy();
     const float* scales = lane < 16 ? qa.k_scales : qa.v_scales;
     int issued = 0;
-    for (int i = 0; i < n_tiles; ++i) {
+    for (int i = part; i < n_tiles; i += C::kProducers) {
       const int st = i % C::kStages;
       if (i >= C::kStages) {
         int go = 1;
@@ -443,7 +456,8 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8>::kThreads, QuantCfg<D, NT8>::
     }
     // this CTA's copies in flight have landed before the warp exits
     for (int i = max(0, issued - C::kStages); i < issued; ++i)
-      mbar_wait_hot(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1);
+      if (i % C::kProducers == part)
+        mbar_wait_hot(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1);
     return;
   }
 

@@ -225,3 +225,26 @@ def test_binding_checks_offsets_and_tables(pkg):
                          (x["t"], x["lens"].long(), TypeError)):
         with pytest.raises(exc):
             pkg._check_table(t, lens, dev)
+
+
+@pytest.mark.parametrize("heads,T,page,D,cluster", [
+    ((64, 8), 1, 64, 128, True),     # 8 rows of one head
+    ((64, 8), 1, 16, 128, False),    # 16 rows of two heads
+    ((64, 8), 2, 64, 128, False),    # 16 rows of one head
+    ((64, 8), 1, 64, 64, True),      # half the bytes
+    ((64, 8), 2, 64, 64, True),      # 16 rows of 64: 4.6 KB, 5.0 KB of room
+    ((64, 8), 1, 16, 64, False),     # 5.1 KB
+    ((64, 8), 1, 16, 256, True),     # one CTA per SM either way
+])
+def test_cluster_plans_leave_room_for_both_ctas(pkg, heads, T, page, D, cluster):
+    """An automatic plan merges through a cluster only where its receive buffer
+    (rows x D fp32) fits beside the rings of the CTAs of an SM."""
+    p = params(pkg, batch=8, num_q_heads=heads[0], num_kv_heads=heads[1], head_dim=D,
+               page_size=page, max_pages_per_seq=16384 // page, num_pages=8 * 16384 // page,
+               max_seq_len=16384, num_queries=T)
+    plan = pkg.decode_attn_quant_make_plan(p, SMS)
+    assert plan.split == 1 and plan.max_shards > 1
+    if cluster:
+        assert plan.cluster == plan.max_shards
+    else:
+        assert plan.cluster == 0
