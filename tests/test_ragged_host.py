@@ -231,7 +231,6 @@ def test_binding_checks_offsets_and_tables(pkg):
     ((64, 8), 1, 64, 128, True),     # 8 rows of one head
     ((64, 8), 1, 16, 128, False),    # 16 rows of two heads
     ((64, 8), 2, 64, 128, False),    # 16 rows of one head
-    ((56, 7), 1, 64, 64, True),      # 8 rows of one head (an odd number of heads)
     ((64, 8), 2, 64, 64, True),      # 16 rows of 64: 4.6 KB, 5.0 KB of room
     ((64, 8), 1, 16, 64, False),     # 5.1 KB
     ((64, 8), 1, 16, 256, True),     # one CTA per SM either way
