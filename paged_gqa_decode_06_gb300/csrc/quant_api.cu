@@ -15,6 +15,8 @@ constexpr int kDefaultSplitMin = 256;
 constexpr int kMinChunk = 128;
 constexpr int kLargeChunkCap = 2048;
 constexpr int64_t kPairBytes = 64 << 20;
+constexpr int kFewSequences = 4;
+constexpr double kSmallStep = 1280 * 1024;  // bytes per SM
 constexpr double kSmRingBytes = 192 * 1024;  // in flight per SM
 // The one-wave cost model of the 16-bit planner: the read rate, the loaded
 // round trip in which a CTA moves its ring, the merge per 8 shards, and the
@@ -31,9 +33,9 @@ size_t ticket_bytes(const decode_attn_params* p) {
 
 // KV heads of a CTA: two where the box of a page's piece of one head is at most
 // 4 KB and the step is large (QuantArgs).  With boxes of 8 KB it depends on the
-// plan (four sequences of 131072 positions 191 -> 185 us, one of them 58 -> 72,
-// eight of 16384 52 -> 113: half the units, so twice the shards to merge), and
-// a small step has too few CTAs as it is.
+// plan (four sequences of 131072 positions 198 -> 191 us, one of them 61 -> 75:
+// half the units, so twice the shards to merge), and a small step has too few
+// CTAs as it is.
 int heads_per_cta(const decode_attn_params* p, int64_t span) {
   const int rows = queries(p) * (p->num_q_heads / p->num_kv_heads);
   const int64_t box = (int64_t)std::min(p->page_size, kTile) * p->head_dim;
@@ -103,9 +105,17 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
     chunk = std::min(round_up(span, kTile), max_chunk);
   } else {
     int64_t s;
-    if (2 * units <= (int64_t)(kOneWaveFill * (double)slots)) {
+    // One wave of equal shards is the quickest where the sequences are equally
+    // long, and the host knows only their bound; where a large step has more
+    // than a few, pieces that the SMs take as they come cost little then and
+    // save much otherwise (16 sequences of 32768, head_dim 64: 63 us by one
+    // wave, 68 by pieces; of U[1, 32768] 55 and 37 us.  8 of 65536, 64 heads:
+    // 198 and 190 us).
+    const double bytes = (double)units * span * row_bytes;
+    const bool several = 2 * units <= (int64_t)(kOneWaveFill * (double)slots);
+    if (several && (bytes <= num_sms * kSmallStep || p->batch <= kFewSequences)) {
       s = one_wave(units, slots, span, row_bytes, max_chunk, kSmRingBytes / ctas_per_sm);
-    } else if ((double)units * span * row_bytes <= (double)slots * (1 << 20)) {
+    } else if (!several && bytes <= (double)slots * (1 << 20)) {
       s = std::max<int64_t>(1, std::min(slots / units, ceil_div(span, kMinChunk)));
     } else {
       // about 1.7 waves; pieces short enough to balance mixed lengths
@@ -140,11 +150,14 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
   // (16 rows of head_dim 128 do not: 8 sequences of 65536, pages of 16, 346 us
   // by clusters, one CTA per SM, and 195 us through the workspace)
   const int recv = ClusterRecv::of(T * G * HC, D, (int)std::min<int64_t>(shards, 16)).bytes;
+  // One CTA per SM leaves GPCs without room for a second cluster of 8 (2
+  // sequences of 16384, head_dim 256: 50 us by clusters, 30 us without).
   const bool cluster_ok =
       plan->split && one_wave_grid && (shards <= 8 || (shards <= 16 && ctas <= 64));
   if (p->schedule == DECODE_ATTN_SCHEDULE_CLUSTER && !cluster_ok) return DECODE_ATTN_ERR_VARIANT;
   if (p->schedule == DECODE_ATTN_SCHEDULE_CLUSTER ||
       (p->schedule == DECODE_ATTN_SCHEDULE_AUTO && cluster_ok &&
+       (ctas_per_sm > 1 || shards <= 4 || ctas <= 64) &&
        recv <= (D == 64 ? QuantCfg<64>::kRecvRoom
                         : D == 128 ? QuantCfg<128>::kRecvRoom : QuantCfg<256>::kRecvRoom) &&
        (ctas * 5 >= slots * 4 || (double)units * span * row_bytes <= (double)(32 << 20))))

@@ -233,17 +233,34 @@ def test_binding_checks_offsets_and_tables(pkg):
     ((64, 8), 2, 64, 128, False),    # 16 rows of one head
     ((64, 8), 2, 64, 64, True),      # 16 rows of 64: 4.6 KB, 5.0 KB of room
     ((64, 8), 1, 16, 64, False),     # 5.1 KB
-    ((64, 8), 1, 16, 256, True),     # one CTA per SM either way
+    ((64, 8), 1, 16, 256, False),    # one CTA per SM: no clusters of 8 on a full grid
 ])
 def test_cluster_plans_leave_room_for_both_ctas(pkg, heads, T, page, D, cluster):
     """An automatic plan merges through a cluster only where its receive buffer
     (rows x D fp32) fits beside the rings of the CTAs of an SM."""
     p = params(pkg, batch=8, num_q_heads=heads[0], num_kv_heads=heads[1], head_dim=D,
-               page_size=page, max_pages_per_seq=16384 // page, num_pages=8 * 16384 // page,
-               max_seq_len=16384, num_queries=T)
+               page_size=page, max_pages_per_seq=8192 // page, num_pages=8 * 8192 // page,
+               max_seq_len=8192, num_queries=T)
     plan = pkg.decode_attn_quant_make_plan(p, SMS)
     assert plan.split == 1 and plan.max_shards > 1
     if cluster:
         assert plan.cluster == plan.max_shards
     else:
         assert plan.cluster == 0
+
+
+def test_long_steps_of_several_sequences_are_cut_into_pieces(pkg):
+    """One wave of equal shards for a few sequences, pieces in the order the
+    SMs take them where more may differ in length."""
+    def ctas(batch, ctx):
+        p = params(pkg, batch=batch, num_q_heads=16, num_kv_heads=4, head_dim=64, page_size=32,
+                   max_pages_per_seq=ctx // 32, num_pages=batch * ctx // 32, max_seq_len=ctx)
+        plan = pkg.decode_attn_quant_make_plan(p, SMS)
+        return plan.grid_x * plan.grid_y * plan.grid_z, 2 * SMS
+
+    for batch, ctx in ((4, 131072), (2, 65536), (16, 8192)):
+        n, slots = ctas(batch, ctx)
+        assert n <= slots
+    for batch, ctx in ((16, 32768), (8, 131072)):
+        n, slots = ctas(batch, ctx)
+        assert n > 1.5 * slots
