@@ -358,7 +358,7 @@ int decode_attn_chunk(const decode_attn_params* p, int32_t total_queries, const 
  * scale, the code the nearest e4m3 number to x / scale (ties to even); a row
  * whose largest magnitude is below 2^-100 becomes zeros with scale 0.  A NaN
  * becomes a NaN code; an Inf takes its row's scale to 2^120 and reads back as
- * Inf, the row's finite values as 0.
+ * Inf, the row's finite values in that scale's steps (0 below 2^110).
  * A row before position 0 (n_b > seq_lens[b]) is not written; a position past
  * the table or a negative length raises DECODE_ATTN_DEV_BAD_LEN, a page id
  * outside [0, P) DECODE_ATTN_DEV_BAD_PAGE, and such a row is not written.

@@ -531,7 +531,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     int edges = 0;
     for (int j = 0; j < ntiles; ++j) {
       if (!edge(j)) continue;
-      if (!mbar_wait_hot(smem_u32(&bar.v_edge), edges & 1)) sh.abort = 1;
+      // (65536 tiles take a tenth of a second, a 2^30-position range all of 8
+      // million: the first edge tile may be the last of them)
+      if (!mbar_wait_long(smem_u32(&bar.v_edge), edges & 1, 1 + (ntiles >> 16))) sh.abort = 1;
       if (!__all_sync(0xffffffffu, !*(volatile int32_t*)&sh.abort)) break;
       const int k0 = key0 + j * KT;
       uint8_t* vt = ring + ((2 * j + 1) % NR) * C::kTileBytes;

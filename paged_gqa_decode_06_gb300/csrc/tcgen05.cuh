@@ -10,9 +10,8 @@
 namespace pgd {
 
 // mbar_wait for waits in a pipeline's inner loop: the clock is read once in
-// 1024 tries only, since a read between two tries delays the wake-up (a
-// prompt of 8192 tokens with it in every turn: see chunk_attn.cuh).  Gives up
-// after about two seconds as mbar_wait does.
+// 1024 tries only, since a read between two tries delays the wake-up.  Gives
+// up after about two seconds as mbar_wait does.
 __device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
@@ -23,6 +22,13 @@ __device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity) {
       if (t - t0 > 2000000000ull) return false;
     }
   }
+}
+
+// The same with a limit `times` as long, for a wait over many steps.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, int times) {
+  while (!mbar_wait_hot(bar, parity))
+    if (--times <= 0) return false;
+  return true;
 }
 
 // Tensor memory: `ncols` (a power of two, at least 32) columns of 128 lanes,
