@@ -95,6 +95,7 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
   const int ctas_per_sm = D == 256 ? QuantCfg<256>::kCtas : QuantCfg<128>::kCtas;
   const int64_t slots = (int64_t)num_sms * ctas_per_sm;
   const double row_bytes = HC * (2.0 * D + 8);  // a position's K and V codes and scales
+  const double bytes = (double)units * span * row_bytes;
   const int split_min = p->split_min > 0 ? p->split_min : kDefaultSplitMin;
 
   int64_t chunk;
@@ -111,7 +112,6 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
     // save much otherwise (16 sequences of 32768, head_dim 64: 63 us by one
     // wave, 68 by pieces; of U[1, 32768] 55 and 37 us.  8 of 65536, 64 heads:
     // 198 and 190 us).
-    const double bytes = (double)units * span * row_bytes;
     const bool several = 2 * units <= (int64_t)(kOneWaveFill * (double)slots);
     if (several && (bytes <= num_sms * kSmallStep || p->batch <= kFewSequences)) {
       s = one_wave(units, slots, span, row_bytes, max_chunk, kSmRingBytes / ctas_per_sm);
@@ -136,19 +136,18 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
   plan->chunk_tokens = (int32_t)chunk;
   plan->max_shards = (int32_t)shards;
   plan->split = shards > 1 ? 1 : 0;
-  plan->head_fastest = one_wave_grid ? 0 : 1;
   plan->balanced = plan->split && one_wave_grid && p->force_chunk <= 0 ? 1 : 0;
-  plan->grid_x = plan->head_fastest ? kv_heads : (int32_t)shards;
-  plan->grid_y = plan->head_fastest ? (int32_t)shards : kv_heads;
-  plan->grid_z = p->batch;
   plan->ctas_per_sm = ctas_per_sm;
   plan->ring_stages = D == 64 ? QuantCfg<64>::kStages
                               : D == 128 ? QuantCfg<128>::kStages : QuantCfg<256>::kStages;
   // the merge, by the 16-bit planner's rule: a cluster for one-wave plans of
-  // 2..8 shards (16 on grids of at most 64 CTAs) that fill 4/5 of the slots
-  // or are small, where the receive buffer leaves room for the CTAs of an SM
-  // (16 rows of head_dim 128 do not: 8 sequences of 65536, pages of 16, 346 us
-  // by clusters, one CTA per SM, and 195 us through the workspace)
+  // 2..8 shards (16 on grids of at most 64 CTAs) that fill 4/5 of the slots,
+  // or of small steps.  Not of long ones, where a cluster's CTAs, shards of one
+  // head, start together and not the heads (four sequences of 131072: 198 us;
+  // 16 of 4096: 33 us, without clusters 35); and only where the receive buffer
+  // leaves room for the CTAs of an SM (16 rows of head_dim 128 do not: 8
+  // sequences of 65536, pages of 16, 346 us by clusters, one CTA per SM, and
+  // 195 us through the workspace)
   const int recv = ClusterRecv::of(T * G * HC, D, (int)std::min<int64_t>(shards, 16)).bytes;
   // One CTA per SM leaves GPCs without room for a second cluster of 8 (2
   // sequences of 16384, head_dim 256: 50 us by clusters, 30 us without).
@@ -160,8 +159,17 @@ extern "C" int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t 
        (ctas_per_sm > 1 || shards <= 4 || ctas <= 64) &&
        recv <= (D == 64 ? QuantCfg<64>::kRecvRoom
                         : D == 128 ? QuantCfg<128>::kRecvRoom : QuantCfg<256>::kRecvRoom) &&
-       (ctas * 5 >= slots * 4 || (double)units * span * row_bytes <= (double)(32 << 20))))
+       ((ctas * 5 >= slots * 4 && bytes <= (double)(256 << 20)) ||
+        bytes <= (double)(32 << 20))))
     plan->cluster = (int32_t)shards;
+  // The heads of a shard side by side: their rows of a position are neighbours
+  // in memory, which the DRAM answers better when they are asked for together
+  // (four sequences of 131072: 192 us, 207 with the shards side by side, as a
+  // cluster's have to be).
+  plan->head_fastest = plan->cluster ? 0 : 1;
+  plan->grid_x = plan->head_fastest ? kv_heads : (int32_t)shards;
+  plan->grid_y = plan->head_fastest ? (int32_t)shards : kv_heads;
+  plan->grid_z = p->batch;
   if (plan->split) {
     const size_t rows = (size_t)p->batch * T * p->num_q_heads * (size_t)shards;
     plan->workspace_bytes =
