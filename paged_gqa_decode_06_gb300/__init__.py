@@ -579,23 +579,25 @@ def _kv_pools(k_pages, v_pages, k_scales, v_scales, index: int) -> int:
     scales an 8-bit pair needs)."""
     if not isinstance(k_pages, torch.Tensor):
         raise TypeError("k_pages must be a torch.Tensor")
-    quant = k_pages.dtype is torch.float8_e4m3fn
-    dt = k_pages.dtype if quant else _elem_dtype(k_pages)
+    dt, shape = k_pages.dtype, k_pages.shape
+    quant = dt is torch.float8_e4m3fn
+    if not quant:
+        _elem_dtype(k_pages)
     _need(k_pages, dt, "k_pages", index)
     _need(v_pages, dt, "v_pages", index)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [P, PS, Hkv, D], both of one shape")
     if not quant:
         if k_scales is not None or v_scales is not None:
             raise ValueError("k_scales and v_scales go with float8_e4m3fn pools only")
         return KV_16BIT
-    P, PS, Hkv, _ = k_pages.shape
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t is None:
-            raise ValueError(f"float8_e4m3fn pools need {name}")
-        _need(t, torch.float32, name, index)
-        if t.shape != (P, Hkv, PS):
-            raise ValueError(f"{name} must be [P, Hkv, PS] = [{P}, {Hkv}, {PS}]")
+    if k_scales is None or v_scales is None:
+        raise ValueError("float8_e4m3fn pools need k_scales and v_scales")
+    _need(k_scales, torch.float32, "k_scales", index)
+    _need(v_scales, torch.float32, "v_scales", index)
+    want = (shape[0], shape[2], shape[1])
+    if k_scales.shape != want or v_scales.shape != want:
+        raise ValueError(f"k_scales and v_scales must be [P, Hkv, PS] = {list(want)}")
     return KV_E4M3
 
 
@@ -636,7 +638,7 @@ def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, 
     sequence owns keep what they held (a new ``out`` is not initialised).
     ``max_seq_len`` (a host-side bound) only steers the plan."""
     index = _cuda_index(q, "q", "decode_attn_chunk")
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens,
                                      scale, window, out, max_seq_len, workspace, err_flag,
@@ -686,7 +688,7 @@ def decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages
     codes, and k_scales/v_scales [P, Hkv, PS] float32 a power of two per row
     and head."""
     index = _cuda_index(k_pages, "k_pages", "decode_kv_append_chunk")
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return decode_kv_append_chunk(k_new, v_new, row_offsets, seq_lens, k_pages, v_pages,
                                           page_table, k_scales, v_scales, err_flag, stream)
@@ -720,7 +722,7 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
     or k_out / v_out as given; rows that no sequence owns keep what they held
     (new outputs are not initialised)."""
     index = _cuda_index(k_pages, "k_pages", "decode_kv_read")
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows, starts,
                                   k_scales, v_scales, dtype, k_out, v_out, err_flag, stream)
@@ -786,7 +788,7 @@ def decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_l
     scale).  q [B, Hq, D] (or [B, T, Hq, D]) fp16 or bf16; returns ``out``
     like q."""
     index = _cuda_index(q, "q", "decode_attn_quant")
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table,
                                      seq_lens, scale, window, out, max_seq_len, workspace,
