@@ -39,7 +39,7 @@
 // fp32.
 //
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 350 us, 1.57
-// PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.62 PFLOP/s (3.05 ms
+// PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.61 PFLOP/s (3.05 ms
 // run after run, where the power limit lowers the clock); at head_dim 256 with a
 // window of 1024, three times 1001 tokens, 75 us, 0.67 PFLOP/s.  What bounds it:
 // a pair of 128 x 128 tiles takes about 2670 cycles of the tensor cores' 2140
