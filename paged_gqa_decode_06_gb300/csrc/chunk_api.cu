@@ -40,6 +40,14 @@ int streams(int head_dim) {
   return head_dim == 256 ? ChunkCfg<256>::kStreams : ChunkCfg<128>::kStreams;
 }
 
+// The window, 0 for none; one as long as the table's capacity is none, so that
+// the kernel's positions minus a window stay in 32 bits (a token before
+// position 0 has a negative one).
+int32_t window_of(const decode_attn_params* p) {
+  const int64_t capacity = (int64_t)p->max_pages_per_seq * p->page_size;
+  return p->window > 0 && p->window < capacity ? p->window : 0;
+}
+
 int run_chunk(const decode_attn_params* p, const decode_attn_chunk_plan& plan, int32_t total,
               const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
               const int32_t* query_offsets, const int32_t* seq_lens, void* out, void* workspace,
@@ -63,7 +71,7 @@ int run_chunk(const decode_attn_params* p, const decode_attn_chunk_plan& plan, i
   a.page_size = p->page_size;
   a.page_shift = ilog2(p->page_size);
   a.box_t = std::min(p->page_size, tile_keys(D));
-  a.window = p->window > 0 ? p->window : 0;
+  a.window = window_of(p);
   a.tile_tok = plan.tile_tokens;
   a.item_tok = plan.item_tokens;
   a.slots = plan.slots;
@@ -138,6 +146,7 @@ extern "C" int decode_attn_chunk_make_plan(const decode_attn_params* p, int32_t 
   plan->item_tokens = NS * plan->tile_tokens;
   const int64_t slots = (int64_t)total_queries / plan->item_tokens + p->batch;
   const int64_t capacity = (int64_t)p->max_pages_per_seq * p->page_size;
+  const int32_t window = window_of(p);
   const int64_t max_len =
       p->max_seq_len > 0 ? std::min<int64_t>(p->max_seq_len, capacity) : capacity;
 
@@ -147,8 +156,8 @@ extern "C" int decode_attn_chunk_make_plan(const decode_attn_params* p, int32_t 
       1, (int64_t)p->batch * ceil_div(avg, plan->item_tokens) * p->num_kv_heads);
   const int64_t tokens = std::min<int64_t>(avg, plan->item_tokens);
   const int64_t span =
-      p->window > 0 ? std::min<int64_t>(max_len, (int64_t)p->window + tokens) : max_len;
-  const int64_t tiles = std::max<int64_t>(1, ceil_div(span, KT) + (p->window > 0 ? 1 : 0));
+      window > 0 ? std::min<int64_t>(max_len, (int64_t)window + tokens) : max_len;
+  const int64_t tiles = std::max<int64_t>(1, ceil_div(span, KT) + (window > 0 ? 1 : 0));
   const int ns = tokens > plan->tile_tokens ? NS : 1;
 
   int64_t shards = 1;

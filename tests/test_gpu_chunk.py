@@ -179,6 +179,15 @@ def test_chunk_tokens_before_position_zero(pkg):
     assert torch.all(got[:4] == 0) and bool((got[4:] != 0).any())
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 48, 47, 39])
+def test_chunk_windows_beyond_every_position(pkg, window):
+    """Windows as long as the table (48 positions here) and longer attend
+    everything, also where tokens before position 0 come with them."""
+    w, q, off = ragged(233, [5, 40], [9, 40], Hq=8, Hkv=2, D=128, PS=16, max_pages=3)
+    got = check(pkg, w, q, off, window)
+    assert torch.all(got[:4] == 0) and bool((got[4:] != 0).any())
+
+
 @pytest.mark.parametrize("force", [0, 128])
 def test_chunk_bad_lengths_and_pages(pkg, force):
     lens = torch.tensor([300, -1, 5000, 300], dtype=torch.int32)
