@@ -55,7 +55,8 @@ __device__ __forceinline__ int2 place_row(const KvRows& a, int row, int lane, bo
   const int b = warp_search(a.B, row, lane, [&](int i) { return (int64_t)a.offsets[i]; });
   if (b < 0) return make_int2(-1, 0);
   const RowRange r = row_range(a.offsets, b, a.total);
-  if (!r.ok || row >= r.first + r.count) return make_int2(-1, 0);
+  // (with offsets that do not ascend the search may end past the row)
+  if (!r.ok || row < r.first || row >= r.first + r.count) return make_int2(-1, 0);
   *owned = true;
   const int64_t base = a.base ? a.base[b] : 0;
   const int64_t pos = base + (row - r.first) - (kAppend ? r.count : 0);

@@ -135,6 +135,28 @@ def test_append_chunk_refused_rows_write_nothing(pkg, quant):
         assert torch.equal(bits(got[n]), bits(want[n])), n
 
 
+@pytest.mark.parametrize("off", [[0, 8, 9, 10, 2, 20], [0, 8, 9, 2, 3, 20], [3, 9, 9, 12, 1, 20],
+                                 [0, 30, 5, 6, 7, 20], [-4, 4, 8, 12, 16, 20]])
+def test_append_with_offsets_that_do_not_ascend(pkg, off):
+    """Reported, and nothing is written but the rows of the sequences whose own
+    offsets ascend, at their own positions."""
+    lens, PS = [40, 50, 60, 70, 40], 16
+    d, table = pools(325, lens, 2, 64, PS, E4M3)
+    k, v = new_rows(326, 20, 2, 64, F16)
+    mine = torch.zeros(d["k_pages"].shape[:2], dtype=torch.bool)
+    for b, L in enumerate(lens):
+        if 0 <= off[b] <= off[b + 1] <= 20:
+            for pos in range(max(0, L - (off[b + 1] - off[b])), L):
+                mine[table[b, pos // PS], pos % PS] = True
+    got, err = run_append(pkg, d, table, k, v, torch.tensor(off, dtype=torch.int32), lens)
+    assert err == pkg.DEV_BAD_LEN
+    for n in d:
+        x, y = bits(got[n]), bits(d[n])
+        if n.endswith("_scales"):
+            x, y = x.transpose(1, 2), y.transpose(1, 2)
+        assert torch.equal(x[~mine], y[~mine]), n
+
+
 def test_append_quantises_the_edges(pkg):
     """Rows at the scale's border (448 times a power of two and its
     neighbours), the smallest and largest magnitudes, ties, NaN and Inf."""
