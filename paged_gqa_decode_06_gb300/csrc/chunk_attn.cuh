@@ -555,8 +555,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       auto key_of = [&](int e) {  // groups of 8 keys, 1 KB per 64 dims
         return k0 + e / D * 8 + (e % 64) / 8;
       };
-      // keys outside the range: whole groups of 8 and what is left of one
-      if (k0 < it.lo || k0 + KT > it.hi)
+      // keys outside the range become zeros: in a pass of their own, or at
+      // head_dim 256 in the next one (window of 1024 there 74.1 -> 72.4 us; the
+      // prompt at 128, where few tiles have such keys, 350 -> 360)
+      if (NS == 2 && (k0 < it.lo || k0 + KT > it.hi))
         for (int e = first; e < C::kTileBytes / 16; e += 64) {
           const int key = key_of(e);
           if (key < it.lo || key >= it.hi) tile[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -566,6 +568,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
 #pragma unroll 8
       for (int e = first; e < C::kTileBytes / 16; e += 64) {
         const uint4 v = tile[e];
+        if (NS == 1 && (key_of(e) < it.lo || key_of(e) >= it.hi)) {
+          tile[e] = make_uint4(0u, 0u, 0u, 0u);
+          continue;
+        }
         top = max2_nan<E>(max2_nan<E>(top, v.x), max2_nan<E>(v.y, max2_nan<E>(v.z, v.w)));
       }
       if (wild2<E>(top) != 0u)
@@ -739,10 +745,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           }
         }
     };
-    // A thread holds a row, so its stores would touch 32 rows at a time; 128
-    // bytes of each of the warp's rows go through shared memory instead (this
+    // A thread holds a row, so its stores would touch 32 rows at a time; 32
+    // columns of the warp's rows go through shared memory instead (this
     // stream's Q, which no product needs any more; 16-byte chunk c of row r at
-    // c ^ (r & 7)) and out as whole lines, 8 lanes a row.
+    // c ^ (r & 7)) and out 4 lanes a row, 8 for a partial.
     const bool whole = it.shards == 1;
     const float inv = dead || l == 0.f ? 0.f : __fdiv_rn(1.f, l);
     if (!whole && rel >= 0)
