@@ -41,7 +41,7 @@
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 350 us, 1.57
 // PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.61 PFLOP/s (3.05 ms
 // run after run, where the power limit lowers the clock); at head_dim 256 with a
-// window of 1024, three times 1001 tokens, 75 us, 0.67 PFLOP/s.  What bounds it:
+// window of 1024, three times 1001 tokens, 73 us, 0.69 PFLOP/s.  What bounds it:
 // a pair of 128 x 128 tiles takes about 2670 cycles of the tensor cores' 2140
 // (8 products of 128 x 128 x 16 take 520 to 550), the chain of barriers between
 // product, softmax and product being the rest, and a CTA adds 8 us before its
@@ -761,6 +761,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const int row_bytes = whole ? D * 2 : a.max_shards * D * 4;
     const int per_row = whole ? 4 : 8;  // lanes of 16 bytes
     const int chunk = lane & (per_row - 1), first = whole ? lane >> 2 : lane >> 3;
+    int rows4[4];  // the output rows that this lane stores to
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rows4[i] = __shfl_sync(0xffffffffu, rel, (lane >> 2) + 8 * i);
     // (a small loop: a CTA runs it once, and most of its time would be the
     // fetching of unrolled code)
 #pragma unroll 1
@@ -789,11 +792,19 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       __syncwarp();
       uint8_t* at = dst + (whole ? c * 2 : c * 4) + chunk * 16;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = stage[(first + 8 * i) * 8 + (chunk ^ first)];
+          if (rows4[i] >= 0) *reinterpret_cast<uint4*>(at + (size_t)rows4[i] * row_bytes) = v;
+        }
+      } else {
 #pragma unroll 4
-      for (int r = first; r < 32; r += 32 / per_row) {
-        const uint4 v = stage[r * 8 + (chunk ^ (r & 7))];
-        const int to = __shfl_sync(0xffffffffu, rel, r);
-        if (to >= 0) *reinterpret_cast<uint4*>(at + (size_t)to * row_bytes) = v;
+        for (int r = first; r < 32; r += 4) {
+          const uint4 v = stage[r * 8 + (chunk ^ (r & 7))];
+          const int to = __shfl_sync(0xffffffffu, rel, r);
+          if (to >= 0) *reinterpret_cast<uint4*>(at + (size_t)to * row_bytes) = v;
+        }
       }
       __syncwarp();
     }
