@@ -48,12 +48,19 @@ struct ClusterRecv {
   int per;         // items of a slice: ceil(rows * D / 4 / S)
   int acc_bytes;   // S * per float4
   int bytes;       // + S * rows float2
-  __host__ __device__ static ClusterRecv of(int rows, int D, int S) {
-    ClusterRecv c;
+  __host__ __device__ static constexpr ClusterRecv of(int rows, int D, int S) {
+    ClusterRecv c{};
     c.per = (rows * (D / 4) + S - 1) / S;
     c.acc_bytes = S * c.per * 16;
     c.bytes = c.acc_bytes + S * rows * 8;
     return c;
+  }
+  // The most that 16 rows take in clusters of up to 16 CTAs.  The slices are
+  // rounded up, so this is not the 16 CTAs' (15 need 48 to 96 bytes more).
+  __host__ __device__ static constexpr int limit(int D) {
+    int most = 0;
+    for (int S = 1; S <= 16; ++S) most = of(16, D, S).bytes > most ? of(16, D, S).bytes : most;
+    return most;
   }
 };
 
