@@ -164,12 +164,14 @@ size_t decode_attn_workspace_size(const decode_attn_params* p, int device);
  * nothing waits) merges that group's partials in ascending shard order and
  * writes out.  A single-pass plan writes out directly.
  * workspace: device memory of at least decode_attn_workspace_size() bytes,
- * 256-byte aligned, owned by the caller.  Its first 64 KiB (more for plans
- * with over 16384 (sequence, KV head) groups) hold one shard ticket per
- * group, which must be zero when a split launch starts: zero the workspace
- * when allocating it, or call decode_attn_workspace_clear().  Every
- * completed call leaves the tickets zero again, and partials never use that
- * region, so one zeroed buffer serves calls of any shape; after a call that
+ * 256-byte aligned, owned by the caller.  Its first 64 KiB hold one shard
+ * ticket per (sequence, KV head) group, which must be zero when a split
+ * launch starts: zero the workspace when allocating it, or call
+ * decode_attn_workspace_clear().  Every completed call leaves the tickets
+ * zero again, and no call's partials use those 64 KiB; the tickets of groups
+ * from 16384 on lie behind them, and a call that has any clears them itself
+ * (an asynchronous memset before its launch).  So one zeroed buffer serves
+ * calls of any shape; after a call that
  * reported DECODE_ATTN_DEV_TIMEOUT or DECODE_ATTN_DEV_WORKSPACE, clear it
  * before reuse.  The rest of the workspace is scratch.  Calls sharing a
  * workspace must not overlap on the GPU.

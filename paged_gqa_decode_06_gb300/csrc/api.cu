@@ -109,9 +109,12 @@ int check_params(const decode_attn_params* p) {
 }
 
 // The shard tickets (one int32 per (sequence, KV head)) sit in a region at
-// the start of every workspace that partials never use, 64 KiB unless a plan
-// has more groups: a zero-filled workspace therefore stays valid across calls
-// with different shapes, since every completed call leaves its tickets zero.
+// the start of every workspace, 64 KiB unless a plan has more groups.  No
+// call's partials touch the first 64 KiB: a zero-filled workspace therefore
+// stays valid across calls with different shapes, since every completed call
+// leaves its tickets zero.  The tickets behind them, of plans with more than
+// 16384 groups, lie where smaller plans keep partials: a call clears its own
+// before its launch (clear_far_tickets).
 constexpr size_t kTicketRegion = 64 * 1024;
 // Group tickets [B*Hkv] (and 64 spare words).
 size_t ticket_region_bytes(const decode_attn_params* p) {
@@ -131,6 +134,15 @@ int next_pow2(int x) {
 
 namespace pgd {
 int validate_params(const decode_attn_params* p) { return check_params(p); }
+size_t ticket_bytes(const decode_attn_params* p) { return ticket_region_bytes(p); }
+int clear_far_tickets(void* tickets, int64_t groups, cudaStream_t stream) {
+  const size_t used = (size_t)groups * 4;
+  if (used <= kTicketRegion) return DECODE_ATTN_OK;
+  return cudaMemsetAsync(static_cast<char*>(tickets) + kTicketRegion, 0, used - kTicketRegion,
+                         stream) == cudaSuccess
+             ? DECODE_ATTN_OK
+             : DECODE_ATTN_ERR_CUDA;
+}
 size_t simt_smem_bytes(int head_dim) {
   switch (head_dim) {
     case 64: return SimtCfg<64>::kSmemBytes;
@@ -503,6 +515,9 @@ int run_split(const decode_attn_params* p, const decode_attn_plan& plan, const v
   L.stream = stream;
   // the shard tickets are zero on entry: the last CTA of each group clears
   // its own, so a workspace cleared once stays clear across calls
+  if (plan.split && !plan.cluster &&
+      (st = clear_far_tickets(ws.counters, (int64_t)p->batch * p->num_kv_heads, stream)))
+    return st;
   switch (p->head_dim) {
     case 64: return cuda_status(launch_split_d64(L));
     case 128: return cuda_status(launch_split_d128(L));

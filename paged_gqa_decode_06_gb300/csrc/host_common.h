@@ -13,6 +13,12 @@ namespace pgd {
 // head dim, page size, group, dtype, schedule; no device call.
 int validate_params(const decode_attn_params* p);
 
+// Bytes of the shard tickets at the start of a workspace, 64 KiB or more, and
+// the clearing of a call's tickets beyond 64 KiB, where other calls keep
+// partials (api.cu).
+size_t ticket_bytes(const decode_attn_params* p);
+int clear_far_tickets(void* tickets, int64_t groups, cudaStream_t stream);
+
 // SM count of a device, looked up once.
 int device_sms(int device, int* sms);
 

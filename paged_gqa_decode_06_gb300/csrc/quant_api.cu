@@ -10,7 +10,6 @@ using namespace pgd;
 
 namespace {
 
-constexpr size_t kTicketRegion = 64 * 1024;
 constexpr int kDefaultSplitMin = 256;
 constexpr int kMinChunk = 128;
 constexpr int kLargeChunkCap = 2048;
@@ -25,11 +24,6 @@ constexpr double kStreamBytesPerS = 7.0e12, kRoundTripS = 3.0e-6, kMergeStepS = 
 constexpr double kOneWaveFill = 0.85;
 
 int queries(const decode_attn_params* p) { return p->num_queries > 1 ? p->num_queries : 1; }
-
-size_t ticket_bytes(const decode_attn_params* p) {
-  return std::max(kTicketRegion,
-                  (size_t)round_up(((int64_t)p->batch * p->num_kv_heads + 64) * 4, 256));
-}
 
 // KV heads of a CTA: two where the box of a page's piece of one head is at most
 // 4 KB and the step is large (QuantArgs).  With boxes of 8 KB it depends on the
@@ -241,6 +235,10 @@ extern "C" int decode_attn_quant(const decode_attn_params* p, int32_t kv_format,
     a.counters = reinterpret_cast<int32_t*>(base);
     a.ws_ml = reinterpret_cast<float2*>(base + tickets);
     a.ws_acc = reinterpret_cast<float*>(base + tickets + round_up(rows * sizeof(float2), 256));
+    if (!plan.cluster &&
+        (st = clear_far_tickets(base, (int64_t)p->batch * kv_heads,
+                                static_cast<cudaStream_t>(stream))))
+      return st;
   }
   a.Hq = p->num_q_heads;
   a.Hkv = kv_heads;
