@@ -400,7 +400,7 @@ int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total
  * decode_attn_quant_make_plan; variant must be AUTO or MMA.
  * workspace: decode_attn_quant_workspace_size() bytes, with decode_attn's
  * rules (tickets zero on entry, left zero); one zeroed buffer serves both.
- * V scales count with magnitudes of 2^-100 to 2^100 (0 for a zero row).
+ * V scales: magnitudes up to 2^100, 0 for a zero row.
  */
 int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t kv_format, int32_t num_sms,
                                 decode_attn_plan* plan);

@@ -20,9 +20,12 @@
 //    scaled by a power of two to magnitudes below 2, which fp16 holds to
 //    2^-25 of the row's largest, and the scores take the factor back.
 //  * The scales enter in fp32, ks with the scores.  vs goes into the weight
-//    w_t = p_t vs_t: the running maximum is taken over log2(p_t vs_t), so
-//    that w_t <= 1 whatever the magnitude of V, while the sum keeps p_t.  w is
-//    split into an fp16 head and remainder (two products), about 22 bits.
+//    w_t = p_t vs_t: the running maximum is taken over log2(p_t vs_t), less 14,
+//    so that the largest w_t is 2^14 whatever the magnitude of V, while the sum
+//    keeps p_t.  w is split into an fp16 head and remainder (two products),
+//    whose last place is 2^-24: 22 bits of a weight down to 2^-16 of the
+//    largest, 11 down to 2^-28, nothing below 2^-39 (with a largest w of 1 the
+//    weights of a context far below one token's would end at 2^-25).
 //
 // Measured (GB300): four sequences of 131072 positions, 64 heads over 8, 184 to
 // 192 us (6.0 to 5.8 TB/s), 64 of U[1, 8192] 108 to 115 us, one of 3060 8.5 us.  The
@@ -95,13 +98,14 @@ __device__ __forceinline__ uint32_t code_offset(int t, int c, int head, int ps) 
                     r * W + (((c % kChunks) ^ key) << 4));
 }
 
-// log2 of a V scale for the running maximum; clamped, so that a zero row
-// (scale 0) neither wins it nor makes a sum overflow.
+// log2 of a V scale for the running maximum, less 14 (above); clamped, so that
+// a zero row (scale 0) neither wins it nor makes a sum overflow: p is at most
+// 2^104 then, the sum of a shard's 65536 at most 2^120.
 __device__ __forceinline__ float scale_log2_of(float v) {
-  const float a = fminf(fmaxf(fabsf(v), 7.8886e-31f), 1.2677e30f);  // 2^-100, 2^100
+  const float a = fminf(fmaxf(fabsf(v), 8.0779e-28f), 1.2677e30f);  // 2^-90, 2^100
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(a));
-  return y;
+  return y - 14.f;
 }
 
 // One consumer warp's 32 positions of a staged tile (K codes at kt, V codes
