@@ -400,7 +400,11 @@ int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total
  * decode_attn_quant_make_plan; variant must be AUTO or MMA.
  * workspace: decode_attn_quant_workspace_size() bytes, with decode_attn's
  * rules (tickets zero on entry, left zero); one zeroed buffer serves both.
- * V scales: magnitudes up to 2^100, 0 for a zero row.
+ * Any V scale below 2^120 counts as it is.  The weights p * scale are held to
+ * 2^-39 of the largest, and where that one's scale is beyond 2^100 the sum of
+ * the p to scale * 2^-140 of its p.  A row with a scale of 2^120 or more (what
+ * the append writes for one with an Inf) makes the dims Inf in which its code
+ * is not zero; the others keep the other positions' values.
  */
 int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t kv_format, int32_t num_sms,
                                 decode_attn_plan* plan);

@@ -82,7 +82,8 @@ struct QuantCfg {
   static constexpr int kSmemBytes = kRingBytes + 1024;
   // static shared memory (scales, row coordinates, warps' states), and what is
   // left of a CTA's share of the SM's 228 KB for a cluster's receive buffer
-  static constexpr int kTableBytes = kStages * 2 * kTile * 4 + kMaxPieces * 4 + 1104;
+  static constexpr int kTableBytes =
+      kStages * 2 * kTile * 4 + kMaxPieces * 4 + D * 4 + (D == 256 ? 1408 : 1120);
   static constexpr int kRecvRoom = 228 * 1024 / kCtas - 1024 - kSmemBytes - kTableBytes;
 };
 
@@ -98,14 +99,62 @@ __device__ __forceinline__ uint32_t code_offset(int t, int c, int head, int ps) 
                     r * W + (((c % kChunks) ^ key) << 4));
 }
 
-// log2 of a V scale for the running maximum, less 14 (above); clamped, so that
-// a zero row (scale 0) neither wins it nor makes a sum overflow: p is at most
-// 2^104 then, the sum of a shard's 65536 at most 2^120.
+// log2 of a V scale for the running maximum, less 14 (above).  At least that of
+// 2^-90, so that a zero row (scale 0) neither wins it nor makes a sum overflow:
+// p is at most 2^104 then, the sum of a shard's 65536 at most 2^120.  No bound
+// above: the weights of a larger scale would pass fp16's range (an Inf, less
+// itself in the remainder: a row of NaN).  A largest weight of scale 2^119
+// leaves p = 2^-105 in the sum, which holds 2^-21 of that (it ends at 2^-126).
 __device__ __forceinline__ float scale_log2_of(float v) {
-  const float a = fminf(fmaxf(fabsf(v), 8.0779e-28f), 1.2677e30f);  // 2^-90, 2^100
+  const float a = fmaxf(fabsf(v), 0x1p-90f);
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(a));
   return y - 14.f;
+}
+
+// V rows with a scale from here on take no part in the maximum and the
+// products, where the other positions would be left without a weight: the
+// append writes 2^120 for a row with an Inf.  (The test costs the long step 0.6
+// % and the mix 1.3 %; on the scales in shared memory, or ahead of the block, 1
+// to 4.)
+constexpr float kHugeScale = 0x1p120f;
+
+// Dims of the CTA's rows (row g of head hd at hd * GP + g) that an Inf (1), a
+// -Inf (2) or a NaN (both) reaches, kept beside the accumulators: the products
+// would carry them to rows that do not attend them.
+template <int D, int GP, int HC>
+struct QuantWild {
+  uint32_t bits[GP * HC][D / 16];  // two bits per dim
+  int32_t any;
+};
+
+// Notes what position t (row tr of the tile) with a huge scale adds to the rows
+// that attend it: an Inf in the dims whose code is not zero.
+template <int D, int NT8, int HC>
+__device__ __forceinline__ void note_huge_row(QuantWild<D, 8 * NT8, HC>& wild, const uint8_t* kt,
+                                              float scale, int tr, int head, int lane, int t,
+                                              const int (&col_lo)[NT8][2],
+                                              const int (&col_hi)[NT8][2], int ps) {
+  wild.any = 1;
+#pragma unroll 1
+  for (int mi = 0; mi < D / 16; ++mi) {
+    const uint16_t codes = *reinterpret_cast<const uint16_t*>(
+        kt + QuantCfg<D>::kTileBytes + code_offset<D, HC>(tr, mi, head, ps) + 2 * (lane >> 2));
+    const float2 x = ElemOps<__half>::unpack2(e4m3_to_half2(codes));
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float v = (i ? x.y : x.x) * scale;
+      const uint32_t two = v != v ? 3u : v > 0.f ? 1u : v < 0.f ? 2u : 0u;
+      bits |= two << (4 * (lane >> 2) + 2 * i);
+    }
+#pragma unroll
+    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (bits != 0u && t >= col_lo[j][e] && t < col_hi[j][e])
+          atomicOr(&wild.bits[head * 8 * NT8 + 8 * j + 2 * (lane & 3) + e][mi], bits);
+  }
 }
 
 // One consumer warp's 32 positions of a staged tile (K codes at kt, V codes
@@ -120,7 +169,8 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
                                             const uint32_t (&qf)[NT8][D / 16][2],
                                             const float (&col_scale)[NT8][2],
                                             float (&acc)[D / 16][NT8][4], float (&m_run)[NT8][2],
-                                            float (&l_part)[NT8][2], int ps) {
+                                            float (&l_part)[NT8][2], int ps,
+                                            QuantWild<D, 8 * NT8, HC>& wild) {
   using H = ElemOps<__half>;
   const int gid = lane >> 2;
   const int mat = lane >> 3, mrow = lane & 7;
@@ -168,6 +218,22 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
     ks[i] = ks_s[gid + 8 * i];
     vs[i] = vs_s[gid + 8 * i];
     lv[i] = scale_log2_of(vs[i]);
+  }
+  const float top = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
+  if (__any_sync(0xffffffffu, top >= kHugeScale)) {
+    const uint32_t apart = __ballot_sync(0xffffffffu, fabsf(vs_s[lane]) >= kHugeScale);
+    for (uint32_t left = apart; left != 0u; left &= left - 1) {
+      const int t = __ffs(left) - 1;
+      if (tok0 + t >= lo && tok0 + t < hi)
+        note_huge_row<D, NT8, HC>(wild, kt, vs_s[t], t0 + t, head, lane, tok0 + t, col_lo, col_hi,
+                                  ps);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (apart >> (gid + 8 * i) & 1u) {
+        vs[i] = 0.f;
+        lv[i] = scale_log2_of(0.f);
+      }
   }
   uint32_t pb_hi[2][NT8][2], pb_lo[2][NT8][2];
   bool rescale = false;
@@ -305,6 +371,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
   __shared__ float2 ml_s[kWarps][GP];
   __shared__ float cw_s[kWarps][GP];
   __shared__ float2 row_s[GP * HC];
+  __shared__ QuantWild<D, GP, HC> wild_s;
   __shared__ int32_t bad_s;
   __shared__ volatile int32_t abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -325,7 +392,10 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
     fence_mbar_init();
     abort_s = 0;
     bad_s = 0;
+    wild_s.any = 0;
   }
+  for (int i = threadIdx.x; i < GP * HC * (D / 16); i += C::kThreads)
+    wild_s.bits[i / (D / 16)][i % (D / 16)] = 0u;
   __syncthreads();
   if constexpr (CL) cluster_arrive_relaxed();
   grid_dependency_wait();
@@ -524,7 +594,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
       quant_block<D, NT8, HC>(ring + st * C::kStageBytes, &scale_s[st][0][32 * half],
                               &scale_s[st][1][32 * half], t0, head, lane, tok0, lo, hi,
                               tok0 >= max(lo, in_lo) && tok0 + 32 <= min(hi, in_hi), col_lo,
-                              col_hi, qf, col_scale, acc, m_run, l_part, piece_shift);
+                              col_hi, qf, col_scale, acc, m_run, l_part, piece_shift, wild_s);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));
   }
@@ -613,6 +683,17 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
       O.y += c * v.y;
       O.z += c * v.z;
       O.w += c * v.w;
+    }
+    if (wild_s.any) {
+      const uint32_t bits = wild_s.bits[hd * GP + g][q >> 2] >> (8 * (q & 3));
+      auto add = [&](float& o, uint32_t two) {
+        if (two & 1u) o += INFINITY;
+        if (two & 2u) o -= INFINITY;
+      };
+      add(O.x, bits);
+      add(O.y, bits >> 2);
+      add(O.z, bits >> 4);
+      add(O.w, bits >> 6);
     }
     const size_t row = group_row(b, h, rc, a.T, a.G, a.Hq);
     if (!a.split) {

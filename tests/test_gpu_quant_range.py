@@ -69,3 +69,69 @@ def test_small_weights_beside_a_large_one(pkg, D, dtype, kw):  # noqa: F811
     floor = L * 2.0 ** -39 * 448 * float(d["v_scales"].max())
     assert_close(got, ref, mass, dtype, weight, floor)
     assert float(got.double()[:, :, 1:].min()) > 0.5 * float(ref[:, :, 1:].min())
+
+
+@pytest.mark.parametrize("kw", [{}, dict(force_chunk=128, schedule=1),
+                                dict(force_chunk=128, schedule=2)], ids=["auto", "grid", "cluster"])
+@pytest.mark.parametrize("exponent", [99, 106, 112, 118])
+def test_the_largest_v_scales(pkg, exponent, kw):  # noqa: F811
+    """V rows near the top of bf16, all of them or one that few tokens attend:
+    scales of 2^exponent, up to what the append writes for finite rows."""
+    L, D = 600, 128
+    w, q, off = ragged(510, [L], [1], Hq=8, Hkv=2, D=D, PS=16, dtype=BF16)
+    g = torch.Generator().manual_seed(511)
+    k, v = (torch.randn((L, 2, D), generator=g) for _ in range(2))
+    for rows in (slice(None), slice(77, 78)):
+        big = v.double().clone()
+        top = big[rows].abs().amax(-1, keepdim=True)
+        big[rows] = big[rows] / top * 440.0 * 2.0 ** exponent
+        d = pool(w, k, big, q, off)
+        assert float(d["v_scales"].max()) == 2.0 ** exponent
+        got, err = run(pkg, d, 1, scale=0.05, **kw)
+        assert err == 0
+        ref, mass = exact(d, 0.05)
+        size = 0.05 * float((q.double().abs().norm(dim=-1)).max()) * \
+            float(k.double().norm(dim=-1).max() * 1.07)  # codes within 2^-4 of the value
+        # every weight within 2^-20 of the largest is in the sum (2^-22 at 2^118)
+        raw = 0.05 * 1.4427 * torch.einsum("hd,td->ht", q[0].double(), k.double()[:, 0])
+        assert float(raw.max() - raw.min()) < 18
+        # an exponent s + log2(vs) - m of numbers below 128 is off by half a
+        # step of those, 2^-18, where it is taken and where m was
+        assert_close(got, ref, mass, BF16, weight_error(D, size) + 2.0 ** -21 + 2.0 ** -17, 0.0)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("kw", [{}, dict(force_chunk=128, schedule=1),
+                                dict(force_chunk=128, schedule=2)], ids=["auto", "grid", "cluster"])
+def test_a_row_with_an_inf_stays_its_own(pkg, kw, D):  # noqa: F811
+    """A V row with an Inf, appended (scale 2^120, code 448) and attended: that
+    dim is Inf in the rows of its head; the other dims and the rows of other
+    heads are the other tokens' values, to the tolerance of any other cache."""
+    L, Hkv = 600, 2
+    w, q, off = ragged(520, [L], [1], Hq=4, Hkv=Hkv, D=D, PS=16, dtype=BF16)
+    g = torch.Generator().manual_seed(521)
+    k, v = (torch.randn((L, Hkv, D), generator=g).bfloat16() for _ in range(2))
+    v[50, 1, 7], v[599, 1, 7] = float("inf"), float("inf")
+    v[300, 1, 30] = float("-inf")
+    v[301, 0, 11], v[302, 0, 11] = float("inf"), float("-inf")
+    P = w.k_pages.shape[0]
+    codes = [torch.zeros((P, 16, Hkv, D), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
+    scales = [torch.zeros((P, Hkv, 16), device=DEV) for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkg.decode_kv_append_chunk(k.to(DEV), v.to(DEV),
+                               torch.tensor([0, L], dtype=torch.int32, device=DEV),
+                               w.seq_lens.to(DEV), *codes, w.page_table.to(DEV), *scales,
+                               err_flag=err)
+    d = dict(q=q, off=off, table=w.page_table, lens=w.seq_lens, scale=w.scale,
+             k_pages=codes[0].cpu(), v_pages=codes[1].cpu(), k_scales=scales[0].cpu(),
+             v_scales=scales[1].cpu())
+    assert float(d["v_scales"].max()) == 2.0 ** 120
+    got, bits = run(pkg, d, 1, **kw)
+    assert int(err.item()) == bits == 0
+    ref, mass = exact(d, w.scale)
+    assert (got[0, 2:, 7] == float("inf")).all() and (got[0, 2:, 30] == float("-inf")).all()
+    assert torch.isnan(got[0, :2, 11]).all()
+    for x in (got, ref, mass):
+        x[0, 2:, 7] = x[0, 2:, 30] = x[0, :2, 11] = 0.0
+    size = w.scale * float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) * 1.07
+    assert_close(got, ref, mass, BF16, weight_error(D, size) + 2.0 ** -21, 0.0)
