@@ -128,10 +128,11 @@ struct QuantWild {
   int32_t any;
 };
 
-// Notes what position t (row tr of the tile) with a huge scale adds to the rows
-// that attend it: an Inf in the dims whose code is not zero.
+// Notes what position t (row tr of the tile) adds to the rows that attend it
+// beside the products: with a huge scale an Inf in the dims whose code is not
+// zero, with a scale of 0 a NaN where the code is one.
 template <int D, int NT8, int HC>
-__device__ __forceinline__ void note_huge_row(QuantWild<D, 8 * NT8, HC>& wild, const uint8_t* kt,
+__device__ __forceinline__ void note_row(QuantWild<D, 8 * NT8, HC>& wild, const uint8_t* kt,
                                               float scale, int tr, int head, int lane, int t,
                                               const int (&col_lo)[NT8][2],
                                               const int (&col_hi)[NT8][2], int ps) {
@@ -161,7 +162,7 @@ __device__ __forceinline__ void note_huge_row(QuantWild<D, 8 * NT8, HC>& wild, c
 // behind them, ks / vs the scales of its positions), as two blocks of 16:
 // mma_block's counterpart.  They are the tile's positions t0.. of head `head`.
 // inside: every column attends all 32.
-template <int D, int NT8, int HC>
+template <int D, int NT8, int HC, bool MT>
 __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, const float* vs_s,
                                             int t0, int head, int lane, int tok0, int lo, int hi,
                                             bool inside, const int (&col_lo)[NT8][2],
@@ -189,6 +190,36 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
     }
     fence_proxy_async_smem();
     __syncwarp();
+  }
+  if (MT && !inside) {
+    // NaN codes of V become zeros and are noted for the rows that attend them:
+    // a zero weight would carry them to the others
+    uint8_t* vt = kt + QuantCfg<D>::kTileBytes;
+    bool nan = false;
+    for (int c = 0; c < D / 16; ++c) {
+      const uint4 v =
+          *reinterpret_cast<const uint4*>(vt + code_offset<D, HC>(t0 + lane, c, head, ps));
+      for (uint32_t w : {v.x, v.y, v.z, v.w})
+        nan |= __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+    }
+    uint32_t rows = __ballot_sync(0xffffffffu, nan);
+    for (uint32_t left = rows; left != 0u; left &= left - 1) {
+      const int t = __ffs(left) - 1;
+      note_row<D, NT8, HC>(wild, kt, 0.f, t0 + t, head, lane, tok0 + t, col_lo, col_hi, ps);
+    }
+    if (rows != 0u) {
+      __syncwarp();
+      if (nan)
+        for (int c = 0; c < D / 16; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(vt + code_offset<D, HC>(t0 + lane, c, head, ps));
+          uint4 v = *at;
+          for (uint32_t* w : {&v.x, &v.y, &v.z, &v.w})
+            *w &= ~__vcmpeq4(*w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          *at = v;
+        }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
   }
   float sc[2][NT8][4];
 #pragma unroll
@@ -225,7 +256,7 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
     for (uint32_t left = apart; left != 0u; left &= left - 1) {
       const int t = __ffs(left) - 1;
       if (tok0 + t >= lo && tok0 + t < hi)
-        note_huge_row<D, NT8, HC>(wild, kt, vs_s[t], t0 + t, head, lane, tok0 + t, col_lo, col_hi,
+        note_row<D, NT8, HC>(wild, kt, vs_s[t], t0 + t, head, lane, tok0 + t, col_lo, col_hi,
                                   ps);
     }
 #pragma unroll
@@ -351,8 +382,10 @@ __device__ __forceinline__ float load_q_row(const uint16_t* row, bool live, int 
   }
 }
 
-// CL: a cluster plan, as in split_mma_body.
-template <int D, int NT8, class E, bool CL, int HC>
+// CL: a cluster plan, as in split_mma_body.  MT: several new tokens per sequence
+// (a kernel of its own: with the test in one kernel the steps of single tokens
+// took 0.5 to 1.5 % longer).
+template <int D, int NT8, class E, bool CL, int HC, bool MT>
 __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT8, HC>::kCtas)
     quant_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const QuantArgs qa) {
@@ -590,11 +623,13 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
     if (bad_s || abort_s) break;
     const int t0 = HC == 1 ? 32 * half : 0;
     const int tok0 = shard_lo + i * kStagePos + t0;
-    if (tok0 + 32 > lo && tok0 < hi)
-      quant_block<D, NT8, HC>(ring + st * C::kStageBytes, &scale_s[st][0][32 * half],
-                              &scale_s[st][1][32 * half], t0, head, lane, tok0, lo, hi,
-                              tok0 >= max(lo, in_lo) && tok0 + 32 <= min(hi, in_hi), col_lo,
-                              col_hi, qf, col_scale, acc, m_run, l_part, piece_shift, wild_s);
+    if (tok0 + 32 > lo && tok0 < hi) {
+      const bool inside = tok0 >= max(lo, in_lo) && tok0 + 32 <= min(hi, in_hi);
+      quant_block<D, NT8, HC, MT>(ring + st * C::kStageBytes, &scale_s[st][0][32 * half],
+                                  &scale_s[st][1][32 * half], t0, head, lane, tok0, lo, hi, inside,
+                                  col_lo, col_hi, qf, col_scale, acc, m_run, l_part, piece_shift,
+                                  wild_s);
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));
   }
