@@ -17,8 +17,9 @@
 //    V register of (2 tokens x 2 dims) gives, after two conversions and two
 //    byte permutations, the registers of two output dims.
 //  * The products are fp16 for either element type of q: a bf16 row of q is
-//    scaled by a power of two to magnitudes below 2, which fp16 holds to
-//    2^-25 of the row's largest, and the scores take the factor back.
+//    scaled by a power of two to magnitudes below 2^15 (the largest above
+//    2^14), where fp16 holds all 8 bits of a value down to 2^-31 of the row's
+//    largest and 2^-39 of it absolutely, and the scores take the factor back.
 //  * The scales enter in fp32, ks with the scores.  vs goes into the weight
 //    w_t = p_t vs_t: the running maximum is taken over log2(p_t vs_t), less 14,
 //    so that the largest w_t is 2^14 whatever the magnitude of V, while the sum
@@ -369,8 +370,9 @@ __device__ __forceinline__ float load_q_row(const uint16_t* row, bool live, int 
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // 2^E of the row's largest value (a tiny row stays, an Inf stays Inf)
-    const uint32_t e = min(max((__float_as_uint(amax) >> 23) & 255u, 27u), 253u);
+    // 2^(E - 14) of the row's largest value, 2^E at least (a tiny row stays, an
+    // Inf stays Inf; bf16's largest is scaled to 65280)
+    const uint32_t e = min(max((__float_as_uint(amax) >> 23) & 255u, 27u), 253u) - 14u;
     const float inv = __uint_as_float((254u - e) << 23);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {

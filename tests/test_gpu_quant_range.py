@@ -135,3 +135,26 @@ def test_a_row_with_an_inf_stays_its_own(pkg, kw, D):  # noqa: F811
         x[0, 2:, 7] = x[0, 2:, 30] = x[0, :2, 11] = 0.0
     size = w.scale * float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) * 1.07
     assert_close(got, ref, mass, BF16, weight_error(D, size) + 2.0 ** -21, 0.0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_bf16_query_with_an_outlier(pkg, D):  # noqa: F811
+    """One dim of q far above the others (2^22), where K is zero: the scores are
+    the other dims' alone, which keep bf16's precision."""
+    L = 700
+    w, q, off = ragged(530, [L], [1], Hq=8, Hkv=2, D=D, PS=16, dtype=BF16)
+    g = torch.Generator().manual_seed(531)
+    k, v = (torch.randn((L, 2, D), generator=g) for _ in range(2))
+    q[:, :, 3], k[:, :, 3] = 2.0 ** 22, 0.0
+    d = pool(w, k, v, q, off)
+    got, err = run(pkg, d, 1, scale=0.2)
+    assert err == 0
+    ref, mass = exact(d, 0.2)
+    # sum |q_d k_d| of the dims that count; q in fp16 with its largest at 2^14:
+    # below 2^-9 = 2^(22 - 31) it loses bits, by at most 2^-25 of 2^14 each
+    rest = q.double().clone()
+    rest[:, :, 3] = 0.0
+    kn = float(k.double().norm(dim=-1).max()) * 1.07
+    size = 0.2 * float(rest.norm(dim=-1).max()) * kn
+    lost = 0.2 * kn * D ** 0.5 * 2.0 ** (22 - 39)
+    assert_close(got, ref, mass, BF16, weight_error(D, size) + 2.0 ** -21 + 2 * lost, 0.0)
