@@ -34,9 +34,9 @@
 // zero would carry it to the others.
 //
 // P is rounded once to the element type for the second product (the weights
-// of a row are at most 2^15, in bf16 2^60, and the largest is at least 1, so
-// each keeps that type's relative precision); sums, maxima and accumulators are
-// fp32.
+// of a row are at most 2^15 and the largest is at least 1; in bf16 at most 1 and
+// the largest at least 2^-16, so that large values do not overflow before they
+// are divided by the sum); sums, maxima and accumulators are fp32.
 //
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 350 us, 1.57
 // PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.61 PFLOP/s (3.05 ms
@@ -606,7 +606,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY;
     uint64_t l2 = 0;  // two partial sums
-    constexpr float kGrow = std::is_same<E, __nv_bfloat16>::value ? 60.f : 15.f;
+    // log2 of the weight of the row's largest score when the reference is taken
+    constexpr float kFirst = std::is_same<E, __nv_bfloat16>::value ? -16.f : 0.f;
+    constexpr float kGrow = std::is_same<E, __nv_bfloat16>::value ? 16.f : 15.f;
     bool ok = true;
     auto wait = [&](uint64_t* b, int parity) {
       if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
@@ -672,9 +674,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       // every value keeps its relative precision): the accumulator is seldom
       // rescaled.  So the first weights are made against it while the tile's
       // maximum is still being taken, and made again in the tiles that move it.
-      if (j == 0) m = row_max();
+      if (j == 0) m = row_max() - kFirst;
       uint64_t sum = weigh(0);
-      const float mx = row_max();
+      const float mx = row_max() - kFirst;
       const bool grow = mx > m + kGrow;
       if (__any_sync(0xffffffffu, grow)) {
         const float alpha = grow ? fast_exp2(m - mx) : 1.f;
