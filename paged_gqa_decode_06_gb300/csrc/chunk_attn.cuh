@@ -33,10 +33,17 @@
 // in the epilogue to the rows that attend it, since a product with a weight of
 // zero would carry it to the others.
 //
-// P is rounded once to the element type for the second product (the weights
-// of a row are at most 2^15 and the largest is at least 1; in bf16 at most 1 and
-// the largest at least 2^-16, so that large values do not overflow before they
-// are divided by the sum); sums, maxima and accumulators are fp32.
+// P is rounded once to the element type for the second product, half a step of
+// that type each.  An fp16 weight ends at 2^-24, so the reference that a row's
+// weights are taken against follows its tiles' maxima down as well as up: the
+// largest weight of a tile lies between 2^-6 and 2^15.9, in a row's first tile
+// (where a token that draws all attention tends to be) at 2^12, and a weight is
+// off by at most 2^-19 of its tile's largest, 2^-37 in the first tile, where it
+// is no normal number.  (With a first weight of 1 that is never lowered, a
+// context 2^-25 below its first token is lost: all of the output, if that token
+// has no value of its own.)  bf16 weights have exponents to spare and stay at or
+// below 1, so that large values do not overflow before they are divided by the
+// sum.  Sums, maxima and accumulators are fp32.
 //
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 350 us, 1.57
 // PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.61 PFLOP/s (3.05 ms
@@ -606,9 +613,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY;
     uint64_t l2 = 0;  // two partial sums
-    // log2 of the weight of the row's largest score when the reference is taken
-    constexpr float kFirst = std::is_same<E, __nv_bfloat16>::value ? -16.f : 0.f;
-    constexpr float kGrow = std::is_same<E, __nv_bfloat16>::value ? 16.f : 15.f;
+    // log2 of the largest weight of the row's first tile, of the tile's that the
+    // reference is moved at, and (fp16) how far below the latter a tile's may
+    // fall; tiles 2^-64 of the row's largest and less do not move it down
+    constexpr bool kHalf = !std::is_same<E, __nv_bfloat16>::value;
+    constexpr float kFirst = kHalf ? 12.f : -16.f, kNext = kHalf ? 2.f : -16.f;
+    constexpr float kGrow = (kHalf ? 15.9f : 0.f) - kNext, kFall = 6.f + kNext, kDeep = 64.f;
+    // the row's largest score, less kNext; rows of no token never look for it
+    [[maybe_unused]] float top =
+        tok < a.tile_tok && it.t0 + s * a.tile_tok + tok < te ? -INFINITY : INFINITY;
     bool ok = true;
     auto wait = [&](uint64_t* b, int parity) {
       if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
@@ -669,16 +682,24 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         }
         return sum;
       };
-      // The reference maximum follows only when the weights would grow beyond
-      // kGrow powers of two (which both formats and the 32-bit sums hold, and
-      // every value keeps its relative precision): the accumulator is seldom
-      // rescaled.  So the first weights are made against it while the tile's
-      // maximum is still being taken, and made again in the tiles that move it.
+      // The reference is moved only when a row's weights would leave their
+      // range, and then of every row of the warp that has risen: the
+      // accumulator is seldom rescaled.  So the first weights are made against
+      // it while the tile's maximum is still being taken, and made again in the
+      // tiles that move it.  (fp16, 1024 tokens at 131072: 2795 us as with a
+      // weight of 1 first and 2^15 at most; moving only the rows that leave the
+      // range 3015, at 2^12 each time 2890; window of 1024 at head_dim 256: 77.0
+      // -> 78.4, 81.9 and 80.0.)
       if (j == 0) m = row_max() - kFirst;
       uint64_t sum = weigh(0);
-      const float mx = row_max() - kFirst;
-      const bool grow = mx > m + kGrow;
-      if (__any_sync(0xffffffffu, grow)) {
+      const float mx = row_max() - kNext;
+      bool grow = mx > m + kGrow, fall = false;
+      if constexpr (kHalf) {
+        top = fmaxf(top, mx);
+        fall = mx < m - kFall && mx > top - kDeep;
+      }
+      if (__any_sync(0xffffffffu, grow || fall)) {
+        if constexpr (kHalf) grow = fall || mx > m;
         const float alpha = grow ? fast_exp2(m - mx) : 1.f;
         if (grow) m = mx;
         // O holds the products up to the unit before: rescale it in place

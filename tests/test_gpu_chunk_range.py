@@ -1,5 +1,8 @@
-"""decode_attn_chunk where numbers of very different sizes meet: values near
-the top of bf16 under rising scores, rows whose scores rise apart.  Against the exact softmax in 64 bits."""
+"""decode_attn_chunk where numbers of very different sizes meet: weights far
+below the first tile's largest, values near the top of bf16 under rising
+scores.  Against the exact softmax in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -25,6 +28,80 @@ def assert_close(got, ref, mass, dtype, weight, floor=0.0):
     assert torch.isfinite(g).all()
     over = (g - ref).abs() - tol
     assert float(over.max()) <= 0, (float(over.max()), float((g - ref).abs().max()))
+
+
+@pytest.mark.parametrize("force", [1 << 20, 0, 16384], ids=["one", "auto", "eight"])
+@pytest.mark.parametrize("D,nats,dtype", [(64, 17.5, F16), (128, 17.0, F16), (128, 17.5, F16),
+                                          (256, 17.5, F16), (128, 17.5, BF16)])
+def test_a_context_far_below_its_first_token(pkg, D, nats, dtype, force):  # noqa: F811
+    """A first token that draws the attention (e^nats over the others) and has no
+    value of its own: the output is the small weights' alone."""
+    L, n = 131072, 3
+    w, _, off = ragged(600, [L], [n], Hq=4, Hkv=1, D=D, PS=64, dtype=dtype)
+    g = torch.Generator().manual_seed(601)
+    k = torch.randn((L, 1, D), generator=g) * 0.02
+    v = torch.randn((L, 1, D), generator=g).abs() + 0.25
+    k[0], v[0] = 1.5, 0.0
+    put(w, k, v)
+    q, scale = torch.ones((n, 4, D), dtype=dtype), nats / (1.5 * D)
+    got, err = run(pkg, w, q, off, scale=scale, max_seq_len=L, force_chunk=force)
+    assert err == 0
+    ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], scale)
+    # weights rounded to the type while they are normal numbers: e^-17.5 is
+    # 2^-25.25 (2^-25.6 with the others' spread), 2^-13.6 in the first tile,
+    # where the largest is 2^12, and near the largest in the others; sum |q k|
+    # is the first token's score, all of one sign
+    assert_close(got, ref, mass, dtype, half_step(dtype) + weight_error(D, nats))
+
+
+@pytest.mark.parametrize("force", [1 << 20, 1024], ids=["one", "shards"])
+@pytest.mark.parametrize("nats", [21.0, 26.0, 31.0])
+@pytest.mark.parametrize("D", [128, 256])
+def test_a_context_below_every_fp16_number(pkg, D, nats, force):  # noqa: F811
+    """Weights that fp16 could not hold beside the first token's: those of the
+    other tiles count in full, those of the first token's own tile are lost
+    below 2^-25 where its weight is 2^12.  Values that keep the result in fp16."""
+    L = 8192
+    w, _, off = ragged(602, [L], [1], Hq=4, Hkv=1, D=D, PS=64)
+    g = torch.Generator().manual_seed(603)
+    k = torch.randn((L, 1, D), generator=g) * 0.02
+    v = ((torch.randn((L, 1, D), generator=g).abs() + 0.25) * 15000.0).clamp(max=60000.0)
+    k[0], v[0] = 1.5, 0.0
+    put(w, k, v)
+    q, scale = torch.ones((1, 4, D)).half(), nats / (1.5 * D)
+    got, err = run(pkg, w, q, off, scale=scale, max_seq_len=L, force_chunk=force)
+    assert err == 0
+    ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], scale)
+    tile = v.double()[1:128 if D == 128 else 64].sum(0)[0]
+    own = tile * min(2.0 ** -37, 1.2 * math.exp(-nats))
+    assert_close(got, ref, mass, F16, half_step(F16) + weight_error(D, nats), own)
+
+
+@pytest.mark.parametrize("place", [0, 700, 4095])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_large_weight_between_small_ones(pkg, D, place):  # noqa: F811
+    """A token that draws the attention at the start, inside or at the end of
+    the context, 25 nats over the rest and without a value of its own; the
+    values are large enough for fp16 to hold the result."""
+    L, nats = 4096, 25.0
+    w, _, off = ragged(604, [L], [1], Hq=4, Hkv=1, D=D, PS=32)
+    g = torch.Generator().manual_seed(605)
+    k = torch.randn((L, 1, D), generator=g) * 0.02
+    v = (torch.randn((L, 1, D), generator=g).abs() + 0.25) * 8192.0
+    v = v.clamp(max=60000.0)
+    k[place], v[place] = 1.5, 0.0
+    put(w, k, v)
+    q, scale = torch.ones((1, 4, D)).half(), nats / (1.5 * D)
+    got, err = run(pkg, w, q, off, scale=scale, max_seq_len=L, force_chunk=1 << 20)
+    assert err == 0
+    ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], scale)
+    # e^-25 is 2^-36.07: the tile of the large weight loses what is below 2^-25
+    # where that weight is 2^12 (the first tile) or 2^2
+    tile = 64 if D == 256 else 128
+    first = place // tile * tile
+    own = v.double()[first:first + tile].sum(0)[0]
+    lost = own * min(2.0 ** -37 if first == 0 else 2.0 ** -27, 1.2 * math.exp(-nats))
+    assert_close(got, ref, mass, F16, half_step(F16) + weight_error(D, nats), lost)
 
 
 @pytest.mark.parametrize("force", [0, 384])
