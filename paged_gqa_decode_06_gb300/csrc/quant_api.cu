@@ -188,6 +188,7 @@ extern "C" int decode_attn_quant(const decode_attn_params* p, int32_t kv_format,
   int st = validate_params(p);
   if (st) return st;
   if (kv_format != DECODE_ATTN_KV_E4M3) return DECODE_ATTN_ERR_SHAPE;
+  if (p->batch == 0) return DECODE_ATTN_OK;
   if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !page_table || !seq_lens || !out)
     return DECODE_ATTN_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_scales) ||
@@ -201,7 +202,6 @@ extern "C" int decode_attn_quant(const decode_attn_params* p, int32_t kv_format,
   if (plan.split && (!workspace || workspace_bytes < plan.workspace_bytes ||
                      (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return DECODE_ATTN_ERR_WORKSPACE;
-  if (p->batch == 0) return DECODE_ATTN_OK;
 
   const int D = p->head_dim;
   const int kv_heads = plan.head_fastest ? plan.grid_x : plan.grid_y;
