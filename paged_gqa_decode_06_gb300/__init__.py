@@ -296,6 +296,16 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream
 
 
+def _new_like(t, stream=None):
+    """A new output like ``t`` that a call on ``stream`` fills: allocated on
+    that stream, since memory that the current stream's allocator hands out
+    may still be in use by that stream's earlier work."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _prepare(q, k_pages, v_pages, page_table, seq_lens, out, scale, window, max_seq_len,
              variant, split_min, force_chunk, workspace, schedule=SCHEDULE_AUTO, stream=None):
     import torch
@@ -314,7 +324,7 @@ def _prepare(q, k_pages, v_pages, page_table, seq_lens, out, scale, window, max_
     p = make_params(q, k_pages, page_table, scale, window, max_seq_len, variant, split_min,
                     force_chunk, schedule)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _check(out, et, "out", dev)
     need = decode_attn_workspace_size(p, dev.index if dev.index is not None else
                                       torch.cuda.current_device())
@@ -335,8 +345,8 @@ def decode_attn(q, k_pages, v_pages, page_table, seq_lens, scale: float, window:
     int32, seq_lens [B] int32, all on one CUDA device.  ``window`` > 0 attends
     the last min(L, window) positions.  ``err_flag``: optional int32 device
     tensor of one element that receives DEV_* bits.  Enqueued on ``stream``
-    (default: torch's current stream); does not synchronise.  ``workspace``:
-    by default a zero-filled buffer cached per (device, stream); pass one to
+    (default: torch's current stream), in whose memory a new ``out`` lies; does
+    not synchronise.  ``workspace``: by default a zero-filled buffer cached per (device, stream); pass one to
     keep its fill out of a captured graph."""
     p, out, ws, ws_bytes = _prepare(q, k_pages, v_pages, page_table, seq_lens, out, scale,
                                     window, max_seq_len, variant, split_min, force_chunk,
@@ -480,7 +490,7 @@ def decode_attn_static_scratch(q, k_pages, v_pages, page_table, seq_lens, scale:
                      (page_table, torch.int32, "page_table"), (seq_lens, torch.int32, "seq_lens")):
         _check(t, dt, n, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     _check(out, et, "out", dev)
     p = make_params(q, k_pages, page_table, scale, window, max_seq_len, variant, split_min,
                     force_chunk, schedule)
@@ -659,7 +669,7 @@ def decode_attn_chunk(q, k_pages, v_pages, page_table, query_offsets, seq_lens, 
     if k_pages.shape[3] != D:
         raise ValueError("q and k_pages head_dim differ")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     else:
         _need(out, et, "out", index)
         if out.shape != q.shape:
@@ -747,10 +757,13 @@ def decode_kv_read(k_pages, v_pages, page_table, row_offsets, total_rows: int, s
             _need(t, dtype, name, index)
             if t.shape != shape:
                 raise ValueError(f"{name} must be [total_rows, Hkv, D] = {list(shape)}")
-    if k_out is None:
+    if k_out is None and stream is None:
         k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    elif k_out is None:  # as _new_like
+        with torch.cuda.stream(stream):
+            k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
     if v_out is None:
-        v_out = torch.empty_like(k_out)
+        v_out = _new_like(k_out, stream)
     p = _params(B, k_pages.shape[2], k_pages.shape, page_table.shape[1], 0, 1.0, 0, dtype)
     st = load_library().decode_kv_read(
         ctypes.byref(p), fmt, shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
@@ -810,7 +823,7 @@ def decode_attn_quant(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_l
     if _check_table(page_table, seq_lens, index) != B:
         raise ValueError("page_table must have a row for each sequence of q")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     else:
         _need(out, et, "out", index)
         if out.shape != q.shape:
