@@ -346,8 +346,8 @@ def decode_attn(q, k_pages, v_pages, page_table, seq_lens, scale: float, window:
     the last min(L, window) positions.  ``err_flag``: optional int32 device
     tensor of one element that receives DEV_* bits.  Enqueued on ``stream``
     (default: torch's current stream), in whose memory a new ``out`` lies; does
-    not synchronise.  ``workspace``: by default a zero-filled buffer cached per (device, stream); pass one to
-    keep its fill out of a captured graph."""
+    not synchronise.  ``workspace``: by default a zero-filled buffer cached per
+    (device, stream); pass one to keep its fill out of a captured graph."""
     p, out, ws, ws_bytes = _prepare(q, k_pages, v_pages, page_table, seq_lens, out, scale,
                                     window, max_seq_len, variant, split_min, force_chunk,
                                     workspace, schedule, stream)
