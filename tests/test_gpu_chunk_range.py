@@ -148,3 +148,22 @@ def test_scores_that_rise_row_by_row(pkg, D, dtype):  # noqa: F811
         ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], 0.1)
         size = 0.1 * float(q.double().norm(dim=-1).max() * w.k_pages.double().norm(dim=-1).max())
         assert_close(got, ref, mass, dtype, half_step(dtype) + weight_error(D, size))
+
+
+@pytest.mark.parametrize("exponent", [-60, -100, -112])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_bf16_values(pkg, D, exponent):  # noqa: F811
+    """bf16 values far below fp16's: the first weights of 2^-16 must not take
+    them out of the 32-bit accumulators."""
+    L, n = 700, 30
+    w, q, off = ragged(630, [L], [n], Hq=8, Hkv=2, D=D, PS=16, dtype=BF16)
+    g = torch.Generator().manual_seed(631)
+    k = torch.randn((L, 2, D), generator=g)
+    v = (torch.randn((L, 2, D), generator=g).abs() + 0.5) * 2.0 ** exponent
+    put(w, k, v)
+    got, err = run(pkg, w, q, off)
+    assert err == 0
+    ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], w.scale)
+    size = w.scale * float(q.double().norm(dim=-1).max() * w.k_pages.double().norm(dim=-1).max())
+    # (a 32-bit sum near 2^-128 has steps of 2^-149: 2^-21 of it)
+    assert_close(got, ref, mass, BF16, half_step(BF16) + weight_error(D, size) + 2.0 ** -20)

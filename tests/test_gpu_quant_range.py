@@ -158,3 +158,31 @@ def test_a_bf16_query_with_an_outlier(pkg, D):  # noqa: F811
     size = 0.2 * float(rest.norm(dim=-1).max()) * kn
     lost = 0.2 * kn * D ** 0.5 * 2.0 ** (22 - 39)
     assert_close(got, ref, mass, BF16, weight_error(D, size) + 2.0 ** -21 + 2 * lost, 0.0)
+
+
+def test_an_inf_and_a_nan_with_two_heads_per_cta(pkg):  # noqa: F811
+    """A table long enough that the plan takes two KV heads per CTA: what is
+    beside the products stays with its own head."""
+    L, Hkv, D, cap = 600, 2, 64, 16384
+    w, q, off = ragged(540, [L], [1], Hq=4, Hkv=Hkv, D=D, PS=16, dtype=BF16, max_pages=cap)
+    g = torch.Generator().manual_seed(541)
+    k, v = (torch.randn((L, Hkv, D), generator=g) for _ in range(2))
+    d = pool(w, k, v, q, off)
+    p = pkg.DecodeAttnParams(1, 4, Hkv, D, 16, cap, d["k_pages"].shape[0], 0, 1.0, 0, 0, 0, 0, 1, 1,
+                             0)
+    plan = pkg.decode_attn_quant_make_plan(p, 152)
+    assert (plan.grid_x if plan.head_fastest else plan.grid_y) == 1
+    page, slot = int(d["table"][0, 500 // 16]), 500 % 16
+    d["v_scales"][page, 1, slot] = 2.0 ** 120
+    codes = torch.zeros(D, dtype=torch.uint8)
+    codes[20], codes[21], codes[22] = 0x7e, 0xfe, 0x7f  # 448, -448, NaN
+    d["v_pages"].view(torch.uint8)[page, slot, 1] = codes
+    got, err = run(pkg, d, 1)
+    assert err == 0
+    assert (got[0, 2:, 20] == float("inf")).all() and (got[0, 2:, 21] == float("-inf")).all()
+    assert torch.isnan(got[0, 2:, 22]).all()
+    ref, mass = exact(d, w.scale)
+    for x in (got, ref, mass):
+        x[0, 2:, 20:23] = 0.0
+    size = w.scale * float(q.double().norm(dim=-1).max() * k.double().norm(dim=-1).max()) * 1.07
+    assert_close(got, ref, mass, BF16, weight_error(D, size) + 2.0 ** -21, 0.0)
