@@ -36,14 +36,15 @@
 // P is rounded once to the element type for the second product, half a step of
 // that type each.  An fp16 weight ends at 2^-24, so the reference that a row's
 // weights are taken against follows its tiles' maxima down as well as up: the
-// largest weight of a tile lies between 2^-6 and 2^15.9, in a row's first tile
-// (where a token that draws all attention tends to be) at 2^12, and a weight is
-// off by at most 2^-19 of its tile's largest, 2^-37 in the first tile, where it
-// is no normal number.  (With a first weight of 1 that is never lowered, a
-// context 2^-25 below its first token is lost: all of the output, if that token
-// has no value of its own.)  bf16 weights have exponents to spare and stay at or
-// below 1, so that large values do not overflow before they are divided by the
-// sum.  Sums, maxima and accumulators are fp32.
+// largest weight of a tile lies between 2^-6 and 2^15.9, at 2^2 in a row's first
+// tile, or at 2^12 where one key of it (a first token that draws all attention)
+// outweighs the others 2^10 times.  A weight that is no normal number is off by
+// at most 2^-19, 2^-27 or 2^-37 of its tile's largest.  (With a first weight of
+// 1 that is never lowered, a context 2^-25 below its first token is lost: all of
+// the output, if that token has no value of its own.)  bf16 weights have
+// exponents to spare and stay at or below 1, so that large values do not
+// overflow before they are divided by the sum.  Sums, maxima and accumulators
+// are fp32.
 //
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 350 us, 1.57
 // PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.61 PFLOP/s (3.05 ms
@@ -613,11 +614,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY;
     uint64_t l2 = 0;  // two partial sums
-    // log2 of the largest weight of the row's first tile, of the tile's that the
-    // reference is moved at, and (fp16) how far below the latter a tile's may
-    // fall; tiles 2^-64 of the row's largest and less do not move it down
+    // log2 of the largest weight of a tile at which the reference is taken
+    // (kFirst: of a row's first tile with one key far above the others), of the
+    // largest and (fp16) the least that a later tile's may be before it is taken
+    // again; tiles 2^-64 of the row's largest and less do not move it down
     constexpr bool kHalf = !std::is_same<E, __nv_bfloat16>::value;
-    constexpr float kFirst = kHalf ? 12.f : -16.f, kNext = kHalf ? 2.f : -16.f;
+    constexpr float kFirst = 12.f, kNext = kHalf ? 2.f : -16.f;
     constexpr float kGrow = (kHalf ? 15.9f : 0.f) - kNext, kFall = 6.f + kNext, kDeep = 64.f;
     // the row's largest score, less kNext; rows of no token never look for it
     [[maybe_unused]] float top =
@@ -686,11 +688,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       // range, and then of every row of the warp that has risen: the
       // accumulator is seldom rescaled.  So the first weights are made against
       // it while the tile's maximum is still being taken, and made again in the
-      // tiles that move it.  (fp16, 1024 tokens at 131072: 2795 us as with a
-      // weight of 1 first and 2^15 at most; moving only the rows that leave the
-      // range 3015, at 2^12 each time 2890; window of 1024 at head_dim 256: 77.0
-      // -> 78.4, 81.9 and 80.0.)
-      if (j == 0) m = row_max() - kFirst;
+      // tiles that move it.  (fp16, against weights of 1 first and 2^15 at most
+      // that only move up, which lose small ones: prompt of 8192 351 us, as
+      // before, window of 1024 at head_dim 256 72.0 -> 73.2.  With every row's
+      // first weight at 2^12 363 and 73.4; moving only the rows that leave the
+      // range, 1024 tokens at 131072 6 % longer.)
+      if (j == 0) {
+        m = row_max() - kNext;
+        if constexpr (kHalf) {
+          // one key so far above the others that the sum is its weight, or next
+          // to nothing: their weights get the range they need
+          const float2 s2 = unpair(weigh(0));
+          const float of = (s2.x + s2.y) * 0x1p-2f;  // in weights of the largest, 2^kNext
+          if ((of < 0x1p-10f && m != -INFINITY) || (of > 0.999f && of < 1.f + 0x1p-10f))
+            m -= kFirst - kNext;
+        }
+      }
       uint64_t sum = weigh(0);
       const float mx = row_max() - kNext;
       bool grow = mx > m + kGrow, fall = false;
@@ -702,21 +715,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         if constexpr (kHalf) grow = fall || mx > m;
         const float alpha = grow ? fast_exp2(m - mx) : 1.f;
         if (grow) m = mx;
-        // O holds the products up to the unit before: rescale it in place
-        // (not reached in the first tile, whose maximum is the reference)
-        wait(&bar.o_full[s], (j - 1) & 1);
-        __syncwarp();
-        tc_fence_after();
-        l2 = mul2(l2, pair(alpha, alpha));
+        if (j > 0) {  // (always so: the first tile's maximum is the reference)
+          // O holds the products up to the unit before: rescale it in place
+          wait(&bar.o_full[s], (j - 1) & 1);
+          __syncwarp();
+          tc_fence_after();
+          l2 = mul2(l2, pair(alpha, alpha));
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          const uint32_t at = tmem_o + s * D + lanes + c;
-          tmem_ld16(o, at);
-          tmem_wait_ld();
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            const uint32_t at = tmem_o + s * D + lanes + c;
+            tmem_ld16(o, at);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] *= alpha;
-          tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
+          }
         }
         sum = weigh(0);
       }
