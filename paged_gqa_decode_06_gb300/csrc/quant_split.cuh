@@ -115,9 +115,10 @@ __device__ __forceinline__ float scale_log2_of(float v) {
 
 // V rows with a scale from here on take no part in the maximum and the
 // products, where the other positions would be left without a weight: the
-// append writes 2^120 for a row with an Inf.  (The test costs the long step 0.6
-// % and the mix 1.3 %; on the scales in shared memory, or ahead of the block, 1
-// to 4.)
+// append writes 2^120 for a row with an Inf.  (The test costs the long step 0.9
+// %, the mix 1.3, head_dim 64 5; ahead of the block 2, 4 and 4.  With 16 query
+// rows it goes there, 64 -> 67 us on 16 sequences of 8192, since in the middle
+// it takes the registers of the products: 74.)
 constexpr float kHugeScale = 0x1p120f;
 
 // Dims of the CTA's rows (row g of head hd at hd * GP + g) that an Inf (1), a
@@ -164,7 +165,7 @@ __device__ __forceinline__ void note_row(QuantWild<D, 8 * NT8, HC>& wild, const 
 // mma_block's counterpart.  They are the tile's positions t0.. of head `head`.
 // inside: every column attends all 32.
 template <int D, int NT8, int HC, bool MT>
-__device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, const float* vs_s,
+__device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, float* vs_s,
                                             int t0, int head, int lane, int tok0, int lo, int hi,
                                             bool inside, const int (&col_lo)[NT8][2],
                                             const int (&col_hi)[NT8][2],
@@ -222,6 +223,23 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
       __syncwarp();
     }
   }
+  // notes the rows of a huge scale; a bit per position
+  auto note_huge_rows = [&] {
+    const uint32_t apart = __ballot_sync(0xffffffffu, fabsf(vs_s[lane]) >= kHugeScale);
+    for (uint32_t left = apart; left != 0u; left &= left - 1) {
+      const int t = __ffs(left) - 1;
+      if (tok0 + t >= lo && tok0 + t < hi)
+        note_row<D, NT8, HC>(wild, kt, vs_s[t], t0 + t, head, lane, tok0 + t, col_lo, col_hi, ps);
+    }
+    return apart;
+  };
+  if constexpr (NT8 == 2)
+    if (__any_sync(0xffffffffu, fabsf(vs_s[lane]) >= kHugeScale)) {
+      const uint32_t apart = note_huge_rows();
+      __syncwarp();
+      if (apart >> lane & 1u) vs_s[lane] = 0.f;
+      __syncwarp();
+    }
   float sc[2][NT8][4];
 #pragma unroll
   for (int b = 0; b < 2; ++b)
@@ -251,21 +269,17 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, cons
     vs[i] = vs_s[gid + 8 * i];
     lv[i] = scale_log2_of(vs[i]);
   }
-  const float top = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
-  if (__any_sync(0xffffffffu, top >= kHugeScale)) {
-    const uint32_t apart = __ballot_sync(0xffffffffu, fabsf(vs_s[lane]) >= kHugeScale);
-    for (uint32_t left = apart; left != 0u; left &= left - 1) {
-      const int t = __ffs(left) - 1;
-      if (tok0 + t >= lo && tok0 + t < hi)
-        note_row<D, NT8, HC>(wild, kt, vs_s[t], t0 + t, head, lane, tok0 + t, col_lo, col_hi,
-                                  ps);
-    }
+  if constexpr (NT8 == 1) {
+    const float top = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
+    if (__any_sync(0xffffffffu, top >= kHugeScale)) {
+      const uint32_t apart = note_huge_rows();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (apart >> (gid + 8 * i) & 1u) {
-        vs[i] = 0.f;
-        lv[i] = scale_log2_of(0.f);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (apart >> (gid + 8 * i) & 1u) {
+          vs[i] = 0.f;
+          lv[i] = scale_log2_of(0.f);
+        }
+    }
   }
   uint32_t pb_hi[2][NT8][2], pb_lo[2][NT8][2];
   bool rescale = false;
