@@ -113,7 +113,10 @@ typedef struct decode_attn_params {
                                 T > 1, q and out are [B][T][Hq][D], query t of sequence b
                                 sits at position seq_lens[b] - T + t and attends causally
                                 (up to itself; the window counted from it); needs
-                                T * G <= 16 and the tensor-core variant */
+                                T * G <= 16 and the tensor-core variant.  decode_attn:
+                                a NaN or Inf in a V row that only some of the T
+                                queries attend reaches all of them (decode_attn_chunk
+                                and decode_attn_quant keep it to those that do) */
   int32_t dtype;             /* DECODE_ATTN_DTYPE_*: element format of every 16-bit
                                 tensor; accumulation is fp32 for both */
   int32_t schedule;          /* DECODE_ATTN_SCHEDULE_*; 0 = automatic */
@@ -364,8 +367,9 @@ int decode_attn_chunk(const decode_attn_params* p, int32_t total_queries, const 
  * A row before position 0 (n_b > seq_lens[b]) is not written; a position past
  * the table or a negative length raises DECODE_ATTN_DEV_BAD_LEN, a page id
  * outside [0, P) DECODE_ATTN_DEV_BAD_PAGE, and such a row is not written.
- * Two rows that name the same cell leave either's.  Uses batch, num_kv_heads,
- * head_dim, page_size, max_pages_per_seq, num_pages and dtype of *p (the
+ * Where two rows name the same cell, its content is a mixture of them (codes
+ * and scale may be of different rows); the other cells are right.  Uses batch,
+ * num_kv_heads, head_dim, page_size, max_pages_per_seq, num_pages and dtype of *p (the
  * other fields must still be valid).  Pointers 16-byte aligned.
  */
 int decode_kv_append_chunk(const decode_attn_params* p, int32_t kv_format, int32_t total_rows,
@@ -398,8 +402,12 @@ int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total
  * force_chunk) with k_t = code * scale, likewise v_t, of a
  * DECODE_ATTN_KV_E4M3 pool.  q and out are params.dtype.  The plan is that of
  * decode_attn_quant_make_plan; variant must be AUTO or MMA.
+ * A position that only some of the T queries attend reaches no other, whatever
+ * it holds.
  * workspace: decode_attn_quant_workspace_size() bytes, with decode_attn's
  * rules (tickets zero on entry, left zero); one zeroed buffer serves both.
+ * The process-wide defaults of the 16-bit planner (DECODE_ATTN_SPLIT_MIN and
+ * DECODE_ATTN_FORCE_CHUNK) do not apply here, nor to decode_attn_chunk.
  * Any V scale below 2^120 counts as it is.  The weights p * scale are held to
  * 2^-39 of the largest, and where that one's scale is beyond 2^100 the sum of
  * the p to scale * 2^-140 of its p.  A row with a scale of 2^120 or more (what

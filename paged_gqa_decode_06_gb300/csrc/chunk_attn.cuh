@@ -46,8 +46,8 @@
 // overflow before they are divided by the sum.  Sums, maxima and accumulators
 // are fp32.
 //
-// Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 350 us, 1.57
-// PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.61 PFLOP/s (3.05 ms
+// Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 348 us, 1.58
+// PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.6 PFLOP/s (3.1 ms
 // run after run, where the power limit lowers the clock); at head_dim 256 with a
 // window of 1024, three times 1001 tokens, 73 us, 0.69 PFLOP/s.  What bounds it:
 // a pair of 128 x 128 tiles takes about 2670 cycles of the tensor cores' 2140

@@ -28,8 +28,8 @@
 //    largest, 11 down to 2^-28, nothing below 2^-39 (with a largest w of 1 the
 //    weights of a context far below one token's would end at 2^-25).
 //
-// Measured (GB300): four sequences of 131072 positions, 64 heads over 8, 184 to
-// 192 us (6.0 to 5.8 TB/s), 64 of U[1, 8192] 108 to 115 us, one of 3060 8.5 us.  The
+// Measured (GB300): four sequences of 131072 positions, 64 heads over 8, 187 us
+// (5.9 TB/s; 195 run after run), 64 of U[1, 8192] 109 us, one of 3060 9.1 us.  The
 // copies bound it: with consumers that only release the stages the long step
 // takes 170 to 185 us, since a head's row is one 128-byte line of the eight that
 // lie together.
