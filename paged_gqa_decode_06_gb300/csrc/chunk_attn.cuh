@@ -36,15 +36,17 @@
 // P is rounded once to the element type for the second product, half a step of
 // that type each.  An fp16 weight ends at 2^-24, so the reference that a row's
 // weights are taken against follows its tiles' maxima down as well as up: the
-// largest weight of a tile lies between 2^-6 and 2^15.9, at 2^2 in a row's first
-// tile, or at 2^12 where one key of it (a first token that draws all attention)
-// outweighs the others 2^10 times.  A weight that is no normal number is off by
-// at most 2^-19, 2^-27 or 2^-37 of its tile's largest.  (With a first weight of
-// 1 that is never lowered, a context 2^-25 below its first token is lost: all of
-// the output, if that token has no value of its own.)  bf16 weights have
-// exponents to spare and stay at or below 1, so that large values do not
-// overflow before they are divided by the sum.  Sums, maxima and accumulators
-// are fp32.
+// largest weight of a tile is 2^2 where it is taken (2^12 in a row's first tile
+// with one key far above the others, as a first token that draws all attention
+// is), at most 2^15.9 later, and one tile's maximum alone does not hold it up.  So
+// the weights that are no normal numbers, off by 2^-25, lose at most 2^-8 of
+// what the row has beside its largest tile, and of that tile what is below
+// 2^-27 (2^-37) of its largest.  (With a first weight of 1 that is never lowered,
+// a context 2^-25 below its first token is lost: all of the output, if that token
+// has no value of its own.)  bf16 weights have exponents to spare: they start at
+// 2^-16 (2^-40 when the reference is taken again) and stay at or below 1, so that
+// large values do not overflow before they are divided by the sum.  Sums, maxima
+// and accumulators are fp32.
 //
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 348 us, 1.58
 // PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.6 PFLOP/s (3.1 ms
@@ -614,16 +616,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY;
     uint64_t l2 = 0;  // two partial sums
-    // log2 of the largest weight of a tile at which the reference is taken
-    // (kFirst: of a row's first tile with one key far above the others), of the
-    // largest and (fp16) the least that a later tile's may be before it is taken
-    // again; tiles 2^-64 of the row's largest and less do not move it down
+    // log2 of the weight at which the reference is taken: in a row's first tile
+    // (kLone: with one key far above its others), when it is taken again, and
+    // what a tile may rise over that before
     constexpr bool kHalf = !std::is_same<E, __nv_bfloat16>::value;
-    constexpr float kFirst = 12.f, kNext = kHalf ? 2.f : -16.f;
-    constexpr float kGrow = (kHalf ? 15.9f : 0.f) - kNext, kFall = 6.f + kNext, kDeep = 64.f;
-    // the row's largest score, less kNext; rows of no token never look for it
-    [[maybe_unused]] float top =
+    constexpr float kNext = kHalf ? 2.f : -40.f, kFirst = kHalf ? kNext : -16.f;
+    constexpr float kLone = 12.f, kGrow = (kHalf ? 15.9f : 0.f) - kNext;
+    // fp16: the largest tile maximum of the row beside the one that the reference
+    // was taken at, less kNext.  The reference is taken down to it once it has a
+    // weight below ntiles * 2^-10: the 2^-25 that each of ntiles * 128 weights
+    // may lose are at most 2^-8 of what it brings otherwise.  (Rows of no token
+    // never do.)
+    [[maybe_unused]] float second =
         tok < a.tile_tok && it.t0 + s * a.tile_tok + tok < te ? -INFINITY : INFINITY;
+    [[maybe_unused]] const float low = (float)min(21 - __clz(ntiles), 1) - kNext;
     bool ok = true;
     auto wait = [&](uint64_t* b, int parity) {
       if (ok && !mbar_wait_hot(smem_u32(b), parity)) {
@@ -690,31 +696,39 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       // it while the tile's maximum is still being taken, and made again in the
       // tiles that move it.  (fp16, against weights of 1 first and 2^15 at most
       // that only move up, which lose small ones: prompt of 8192 351 us, as
-      // before, window of 1024 at head_dim 256 72.0 -> 73.2.  With every row's
-      // first weight at 2^12 363 and 73.4; moving only the rows that leave the
-      // range, 1024 tokens at 131072 6 % longer.)
+      // before, with scores twice as sharp 360 -> 386, four times 418 -> 456, where
+      // following every tile down takes 464 and 469; window of 1024 at head_dim
+      // 256 71.7 -> 72.6.  Every row's first weight at 2^12: prompt 363.)
       if (j == 0) {
-        m = row_max() - kNext;
+        m = row_max() - kFirst;
         if constexpr (kHalf) {
           // one key so far above the others that the sum is its weight, or next
           // to nothing: their weights get the range they need
           const float2 s2 = unpair(weigh(0));
           const float of = (s2.x + s2.y) * 0x1p-2f;  // in weights of the largest, 2^kNext
           if ((of < 0x1p-10f && m != -INFINITY) || (of > 0.999f && of < 1.f + 0x1p-10f))
-            m -= kFirst - kNext;
+            m -= kLone - kNext;
         }
       }
       uint64_t sum = weigh(0);
       const float mx = row_max() - kNext;
       bool grow = mx > m + kGrow, fall = false;
       if constexpr (kHalf) {
-        top = fmaxf(top, mx);
-        fall = mx < m - kFall && mx > top - kDeep;
+        if (j > 0) second = fmaxf(second, fminf(m, mx));
+        fall = second < m + low && mx < second + kGrow;
       }
       if (__any_sync(0xffffffffu, grow || fall)) {
-        if constexpr (kHalf) grow = fall || mx > m;
-        const float alpha = grow ? fast_exp2(m - mx) : 1.f;
-        if (grow) m = mx;
+        if (fall) {  // past sums stay below 2^80: tiles 2^-64 of others may vanish
+          const float2 lh = unpair(l2);
+          if ((lh.x + lh.y) * fast_exp2(m - second) > 0x1p80f) {
+            fall = false;
+            second = m;
+          }
+        }
+        const float ref = fall ? second : mx;
+        grow = fall || mx > m;
+        const float alpha = grow ? fast_exp2(m - ref) : 1.f;
+        if (grow) m = ref;
         if (j > 0) {  // (always so: the first tile's maximum is the reference)
           // O holds the products up to the unit before: rescale it in place
           wait(&bar.o_full[s], (j - 1) & 1);

@@ -167,3 +167,25 @@ def test_small_bf16_values(pkg, D, exponent):  # noqa: F811
     size = w.scale * float(q.double().norm(dim=-1).max() * w.k_pages.double().norm(dim=-1).max())
     # (a 32-bit sum near 2^-128 has steps of 2^-149: 2^-21 of it)
     assert_close(got, ref, mass, BF16, half_step(BF16) + weight_error(D, size) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("gap", [40.0, 60.0, 120.0, 400.0])
+def test_towering_keys_at_any_distance(pkg, D, gap, dtype):  # noqa: F811
+    """Keys whose scores stand `gap` powers of two above all others, at two
+    places: sums and accumulators stay finite however far the reference could
+    follow the tiles between them."""
+    L, n = 1400, 20
+    w, _, off = ragged(640, [L], [n], Hq=4, Hkv=1, D=D, PS=16, dtype=dtype)
+    g = torch.Generator().manual_seed(641)
+    k = torch.randn((L, 1, D), generator=g) * 0.02
+    v = torch.randn((L, 1, D), generator=g)
+    k[5], k[700] = 1.0, 1.5
+    put(w, k, v)
+    q, scale = torch.ones((n, 4, D), dtype=dtype), gap * 0.6931 / D
+    for force in (0, 1 << 20):
+        got, err = run(pkg, w, q, off, scale=scale, force_chunk=force)
+        assert err == 0
+        ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], scale)
+        assert_close(got, ref, mass, dtype, half_step(dtype) + weight_error(D, gap * 1.1))
