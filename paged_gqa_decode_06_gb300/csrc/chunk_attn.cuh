@@ -44,9 +44,9 @@
 // 2^-27 (2^-37) of its largest.  (With a first weight of 1 that is never lowered,
 // a context 2^-25 below its first token is lost: all of the output, if that token
 // has no value of its own.)  bf16 weights have exponents to spare: they start at
-// 2^-16 (2^-40 when the reference is taken again) and stay at or below 1, so that
-// large values do not overflow before they are divided by the sum.  Sums, maxima
-// and accumulators are fp32.
+// 2^-16 and stay at or below 1, so that large values do not overflow before they
+// are divided by the sum (2^-40 where scores have risen beyond that: values
+// below 2^-86 lose bits there).  Sums, maxima and accumulators are fp32.
 //
 // Measured (GB300): a prompt of 8192 tokens, 32 heads over 8, 348 us, 1.58
 // PFLOP/s; 1024 tokens at 131072, 64 heads over 8, 2.7 ms, 1.6 PFLOP/s (3.1 ms
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       // it while the tile's maximum is still being taken, and made again in the
       // tiles that move it.  (fp16, against weights of 1 first and 2^15 at most
       // that only move up, which lose small ones: prompt of 8192 351 us, as
-      // before, with scores twice as sharp 360 -> 386, four times 418 -> 456, where
+      // before, with scores twice as sharp 360 -> 390, four times 418 -> 460, where
       // following every tile down takes 464 and 469; window of 1024 at head_dim
       // 256 71.7 -> 72.6.  Every row's first weight at 2^12: prompt 363.)
       if (j == 0) {
@@ -725,8 +725,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
             second = m;
           }
         }
-        const float ref = fall ? second : mx;
-        grow = fall || mx > m;
+        // (a row without a key so far takes its first reference, which in bf16
+        // moves no other row)
+        const bool begins = m == -INFINITY;
+        const bool all = kHalf || __any_sync(0xffffffffu, grow && !begins);
+        const float ref = fall ? second : begins ? mx + (kNext - kFirst) : mx;
+        grow = fall || (ref > m && (all || begins));
         const float alpha = grow ? fast_exp2(m - ref) : 1.f;
         if (grow) m = ref;
         if (j > 0) {  // (always so: the first tile's maximum is the reference)

@@ -115,10 +115,10 @@ __device__ __forceinline__ float scale_log2_of(float v) {
 
 // V rows with a scale from here on take no part in the maximum and the
 // products, where the other positions would be left without a weight: the
-// append writes 2^120 for a row with an Inf.  (The test costs the long step 0.9
-// %, the mix 1.3, head_dim 64 5; ahead of the block 2, 4 and 4.  With 16 query
-// rows it goes there, 64 -> 67 us on 16 sequences of 8192, since in the middle
-// it takes the registers of the products: 74.)
+// append writes 2^120 for a row with an Inf.  (The test takes 0.9 % of the long
+// step's time, 1.3 of the mix's, 5 at head_dim 64; ahead of the block 2, 4 and 4.
+// With 16 query rows it goes there, 64 -> 68 us on 16 sequences of 8192, since
+// in the middle it takes the registers of the products: 74.)
 constexpr float kHugeScale = 0x1p120f;
 
 // Dims of the CTA's rows (row g of head hd at hd * GP + g) that an Inf (1), a
@@ -135,9 +135,9 @@ struct QuantWild {
 // zero, with a scale of 0 a NaN where the code is one.
 template <int D, int NT8, int HC>
 __device__ __forceinline__ void note_row(QuantWild<D, 8 * NT8, HC>& wild, const uint8_t* kt,
-                                              float scale, int tr, int head, int lane, int t,
-                                              const int (&col_lo)[NT8][2],
-                                              const int (&col_hi)[NT8][2], int ps) {
+                                         float scale, int tr, int head, int lane, int t,
+                                         const int (&col_lo)[NT8][2],
+                                         const int (&col_hi)[NT8][2], int ps) {
   wild.any = 1;
 #pragma unroll 1
   for (int mi = 0; mi < D / 16; ++mi) {

@@ -189,3 +189,20 @@ def test_towering_keys_at_any_distance(pkg, D, gap, dtype):  # noqa: F811
         assert err == 0
         ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], scale)
         assert_close(got, ref, mass, dtype, half_step(dtype) + weight_error(D, gap * 1.1))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_bf16_values_behind_a_masked_tile(pkg, D):  # noqa: F811
+    """Windows that leave a CTA's first tile to some of its rows only: the others
+    take their reference in a later one."""
+    L, n, window = 900, 130, 100
+    w, q, off = ragged(650, [L], [n], Hq=2, Hkv=2, D=D, PS=16, dtype=BF16)
+    g = torch.Generator().manual_seed(651)
+    k = torch.randn((L, 2, D), generator=g)
+    v = (torch.randn((L, 2, D), generator=g).abs() + 0.5) * 2.0 ** -112
+    put(w, k, v)
+    got, err = run(pkg, w, q, off, window)
+    assert err == 0
+    ref, mass = chunk_attention(q, w.k_pages, w.v_pages, w.page_table, off, [L], w.scale, window)
+    size = w.scale * float(q.double().norm(dim=-1).max() * w.k_pages.double().norm(dim=-1).max())
+    assert_close(got, ref, mass, BF16, half_step(BF16) + weight_error(D, size) + 2.0 ** -20)
