@@ -409,7 +409,7 @@ int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total
  * The process-wide defaults of the 16-bit planner (DECODE_ATTN_SPLIT_MIN and
  * DECODE_ATTN_FORCE_CHUNK) do not apply here, nor to decode_attn_chunk.
  * Any V scale below 2^120 counts as it is.  The weights p * scale are held to
- * 2^-39 of the largest, and where that one's scale is beyond 2^100 the sum of
+ * 2^-39 of the largest (for which one below 2^-90 counts as that), and where that one's scale is beyond 2^100 the sum of
  * the p to scale * 2^-140 of its p.  A row with a scale of 2^120 or more (what
  * the append writes for one with an Inf) makes the dims Inf in which its code
  * is not zero; the others keep the other positions' values.

@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t code_offset(int t, int c, int head, int ps) 
 }
 
 // log2 of a V scale for the running maximum, less 14 (above).  At least that of
-// 2^-90, so that a zero row (scale 0) neither wins it nor makes a sum overflow:
-// p is at most 2^104 then, the sum of a shard's 65536 at most 2^120.  No bound
+// 2^-90, so that a zero row (scale 0) makes no sum overflow: p is at most 2^104
+// then, the sum of a shard's 65536 at most 2^120.  No bound
 // above: the weights of a larger scale would pass fp16's range (an Inf, less
 // itself in the remainder: a row of NaN).  A largest weight of scale 2^119
 // leaves p = 2^-105 in the sum, which holds 2^-21 of that (it ends at 2^-126).
