@@ -319,6 +319,9 @@ int decode_attn_static_scratch(const decode_attn_params* p, const void* q, const
  * such pages of its tile may, too).  What a token does not attend
  * (later positions, positions before its window, a page's unused ones) never
  * reaches its row, whatever it holds.
+ * The softmax weights are rounded once to the element type.  fp16: beside a key
+ * of the same 128 positions (64 at head_dim 256), aligned, weights below 2^-27
+ * of its weight do not count (2^-37 in the first of them that a row attends).
  * workspace: decode_attn_chunk_workspace_size() bytes, 256-byte aligned;
  * scratch that needs no clearing, 0 bytes for a plan without shards.  It may
  * be a workspace of decode_attn, whose shard tickets (its first 64 KiB) stay
