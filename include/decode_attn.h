@@ -576,9 +576,12 @@ int decode_kv_read_fp4(const decode_attn_params* p, const decode_kv_cache* cache
  * and this).  A position that only some of the T queries attend reaches no
  * other, whatever it holds.
  * The weights p * row are rounded to fp16 once, the largest 2^14: 2^-11 of each
- * down to 2^-28 of the largest, nothing below 2^-39 of it (for which one below
- * 2^-90 counts as that).  plan.ring_stages counts the units of 32 positions of
- * one head in flight per CTA; a CTA takes one KV head or two.  A V row with a scale of 2^120 or more, or a NaN, makes
+ * down to 2^-28 of the largest, nothing below 2^-39 of it (for which a row below
+ * 2^-90 counts as that).  The sum of the p takes every position, however far apart
+ * the row scales lie; among positions that one warp takes (32 of each 128) beside one
+ * whose scale is beyond 2^100, those of p above scale * 2^-140 of its p.
+ * plan.ring_stages counts the units of 32 positions of one head in flight per CTA; a
+ * CTA takes one KV head or two.  A V row with a scale of 2^120 or more, or a NaN, makes
  * the rows that attend it NaN (the append writes at most 2^117).
  */
 int decode_attn_fp4_make_plan(const decode_attn_params* p, int32_t num_sms,

@@ -427,8 +427,8 @@ template <bool kInside, bool kFactor>
 __device__ __forceinline__ bool fp4_weights_4(const float (&sc)[2][2], const float4* rows,
                                               const float (&scale)[2], const int2* col_s,
                                               int tok0, int lane, uint32_t sel,
-                                              float (&m_run)[2], float (&l_part)[2],
-                                              float (&alpha)[2], uint32_t (&wb)[4][2]) {
+                                              float (&m_run)[2], float (&l_sum)[2],
+                                              float (&down)[2], uint32_t (&wb)[4][2]) {
   const int gid = lane >> 2, tig = lane & 3;
   const int first = 8 * (tig & 2) + gid;  // this lane's positions: first, first + 8
   float4 row[2];
@@ -454,16 +454,16 @@ __device__ __forceinline__ bool fp4_weights_4(const float (&sc)[2][2], const flo
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     const float m_new = fmaxf(m_run[e], mx);
-    alpha[e] = (m_new == -INFINITY) ? 1.f : fast_exp2(m_run[e] - m_new);
-    rescale |= alpha[e] != 1.f;
-    float l = l_part[e] * alpha[e];
+    down[e] = (m_new == -INFINITY) ? 0.f : m_run[e] - m_new;
+    rescale |= down[e] != 0.f;
+    float l = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float p = in[i] ? fast_exp2(sv[i] - m_new) : 0.f;
       l += p;
       w[i][e] = in[i] ? p * row[i].y : 0.f;
     }
-    l_part[e] = l;
+    l_sum[e] = l;
     m_run[e] = m_new;
   }
 #pragma unroll
@@ -533,7 +533,7 @@ template <int NQ, int NJ, bool kInside, bool kFactor>
 __device__ __forceinline__ bool fp4_weights(const float (&sc)[2][NJ][4], const float4* rows,
                                             const float (&scale)[NJ][2], const int2* col_s,
                                             int tok0, int lane, float (&m_run)[NJ][2],
-                                            float (&l_part)[NJ][2], float (&alpha)[NJ][2],
+                                            float (&l_sum)[NJ][2], float (&down)[NJ][2],
                                             uint32_t (&wt)[4][NJ]) {
   const int gid = lane >> 2, tig = lane & 3;
   float4 row[4];  // this lane's positions: gid + 8 i
@@ -561,16 +561,16 @@ __device__ __forceinline__ bool fp4_weights(const float (&sc)[2][NJ][4], const f
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       const float m_new = fmaxf(m_run[j][e], mx);
-      alpha[j][e] = (m_new == -INFINITY) ? 1.f : fast_exp2(m_run[j][e] - m_new);
-      rescale |= alpha[j][e] != 1.f;
-      float l = l_part[j][e] * alpha[j][e];
+      down[j][e] = (m_new == -INFINITY) ? 0.f : m_run[j][e] - m_new;
+      rescale |= down[j][e] != 0.f;
+      float l = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p = in[i] ? fast_exp2(sv[i] - m_new) : 0.f;
         l += p;
         w[i][e] = in[i] ? p * row[i].y : 0.f;
       }
-      l_part[j][e] = l;
+      l_sum[j][e] = l;
       m_run[j][e] = m_new;
     }
 #pragma unroll
@@ -923,23 +923,31 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NQ, HC>::kThreads, Fp4Cfg<D, NQ, HC>
     }
     ready_scales<NB>(words, ready_v + lane * 2 * NB);
     uint32_t wt[4][NQ == 4 ? 2 : NJ];
-    float alpha[NJ][2];
+    float l_sum[NJ][2], down[NJ][2];
     constexpr bool kFactor = !std::is_same<E, __half>::value;
     bool rescale;
     auto weights = [&](auto whole) {
       if constexpr (NQ == 4)
         rescale = fp4_weights_4<decltype(whole)::value, kFactor>(
             reinterpret_cast<float(&)[2][2]>(sc), my_rows, scale[0], col_s, tok0, lane, sel,
-            m_run[0], l_part[0], alpha[0], wt);
+            m_run[0], l_sum[0], down[0], wt);
       else
         rescale = fp4_weights<NQ, NJ, decltype(whole)::value, kFactor>(
-            sc, my_rows, scale, col_s, tok0, lane, m_run, l_part, alpha, wt);
+            sc, my_rows, scale, col_s, tok0, lane, m_run, l_sum, down, wt);
     };
     if (inside)
       weights(std::true_type{});
     else
       weights(std::false_type{});
     if (__any_sync(0xffffffffu, rescale)) {
+      float alpha[NJ][2];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          alpha[j][e] = fast_exp2(down[j][e]);
+          l_part[j][e] = carry_sum(l_part[j][e], down[j][e], alpha[j][e]);
+        }
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
 #pragma unroll
@@ -952,6 +960,10 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NQ, HC>::kThreads, Fp4Cfg<D, NQ, HC>
             acc[c][j][p][3] *= alpha[j][1];
           }
     }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l_part[j][e] += l_sum[j][e];
     __syncwarp();
     fp4_values<D, NQ, NJ, NP>(to + v_at, ready_v + vs_at, wt, acc);
     __syncwarp();
@@ -1018,17 +1030,8 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NQ, HC>::kThreads, Fp4Cfg<D, NQ, HC>
   if ((int)threadIdx.x < R) {
     int hd;
     const int g = head_row(threadIdx.x, hd);
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; w += HC) M = fmaxf(M, ml_s[w + hd][g].x);
-    float L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w += HC) {
-      const float2 ml = ml_s[w + hd][g];
-      const float c = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
-      if (ml.y != 0.f) L += c * ml.y;
-      cw_s[w + hd][g] = c;
-    }
+    const float2 ML = fold_states<kWarps, HC, GP>(ml_s, cw_s, hd, g);
+    const float M = ML.x, L = ML.y;
     // (positions whose scores are no numbers alone leave no maximum, and would
     // pass for none in the merge)
     row_s[threadIdx.x] = make_float2(L != L ? fmaxf(M, -3e38f) : M, L);

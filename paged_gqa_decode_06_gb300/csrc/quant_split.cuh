@@ -121,6 +121,58 @@ __device__ __forceinline__ float scale_log2_of(float v) {
 // in the middle it takes the registers of the products: 74.)
 constexpr float kHugeScale = 0x1p120f;
 
+// A row's sum l carried to a larger maximum: l * 2^d, d <= 0, with alpha =
+// exp2(d).  With V scales that far apart (zero rows, whose p is up to 2^104, before
+// a row of 2^40) the factor alone is below fp32's range where the product is not:
+// then in two halves.
+__device__ __forceinline__ float carry_sum(float l, float d, float alpha) {
+  if (alpha != 0.f || l == 0.f) return l * alpha;
+  const float h = fast_exp2(0.5f * d);
+  return l * h * h;
+}
+
+// A row's state before it meets others.  The sum l is relative to a maximum that V's
+// scales have part in, so it can lie anywhere between 2^-106 and 2^121, and the factor
+// between two states' maxima beyond fp32's range.  Where l is that far from 1 the
+// reference moves to the sum's own exponent; returns the factor of l and of the
+// accumulators, which become the values' own size (2^-17 of it where they may be near
+// the end of the range, so that sums over 2^16 states stay in it).  Within 2^+-40, all
+// but such rows, nothing changes: equal shares then differ by 2^80 at most, and 2^-46
+// of a share still counts.
+__device__ __forceinline__ float settle(float& m, float& l) {
+  const int e = (int)(__float_as_uint(l) >> 23) - 126;  // l in [2^(e - 1), 2^e)
+  if (!(l > 0.f) || e > 126 || (e <= 40 && e >= -40)) return 1.f;
+  const int by = e < 0 ? e + 17 : e;
+  const float f = __uint_as_float((uint32_t)(127 - by) << 23);
+  m += (float)by;
+  l *= f;
+  return f;
+}
+
+// The state (m, l) of row g of head hd over the warps that have it, in fixed order, and
+// each warp's factor for its accumulators.
+template <int kWarps, int HC, int GP>
+__device__ __forceinline__ float2 fold_states(const float2 (&ml_s)[kWarps][GP],
+                                              float (&cw_s)[kWarps][GP], int hd, int g) {
+  float m[kWarps / HC], l[kWarps / HC], f[kWarps / HC];
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps / HC; ++w) {
+    const float2 ml = ml_s[HC * w + hd][g];
+    m[w] = ml.x;
+    l[w] = ml.y;
+    f[w] = settle(m[w], l[w]);
+    M = fmaxf(M, m[w]);
+  }
+#pragma unroll
+  for (int w = 0; w < kWarps / HC; ++w) {
+    const float c = l[w] == 0.f ? 0.f : fast_exp2(m[w] - M);
+    if (l[w] != 0.f) L += c * l[w];
+    cw_s[HC * w + hd][g] = c * f[w];
+  }
+  return make_float2(M, L);
+}
+
 // Dims of the CTA's rows (row g of head hd at hd * GP + g) that an Inf (1), a
 // -Inf (2) or a NaN (both) reaches, kept beside the accumulators: the products
 // would carry them to rows that do not attend them.
