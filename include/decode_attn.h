@@ -411,11 +411,12 @@ int decode_kv_read(const decode_attn_params* p, int32_t kv_format, int32_t total
  * rules (tickets zero on entry, left zero); one zeroed buffer serves both.
  * The process-wide defaults of the 16-bit planner (DECODE_ATTN_SPLIT_MIN and
  * DECODE_ATTN_FORCE_CHUNK) do not apply here, nor to decode_attn_chunk.
- * Any V scale below 2^120 counts as it is.  The weights p * scale are held to
- * 2^-39 of the largest (for which one below 2^-90 counts as that), and where that one's scale is beyond 2^100 the sum of
- * the p to scale * 2^-140 of its p.  A row with a scale of 2^120 or more (what
- * the append writes for one with an Inf) makes the dims Inf in which its code
- * is not zero; the others keep the other positions' values.
+ * Any V scale below 2^120 counts as it is, however far apart they lie.  The weights
+ * p * scale are held to 2^-39 of the largest (for which one below 2^-90 counts as
+ * that), and where that one's scale is beyond 2^100 the sum of the p, over the
+ * positions that one warp takes, to scale * 2^-140 of its p.  A row with a scale of
+ * 2^120 or more (what the append writes for one with an Inf) makes the dims Inf in
+ * which its code is not zero; the others keep the other positions' values.
  */
 int decode_attn_quant_make_plan(const decode_attn_params* p, int32_t kv_format, int32_t num_sms,
                                 decode_attn_plan* plan);
@@ -578,8 +579,8 @@ int decode_kv_read_fp4(const decode_attn_params* p, const decode_kv_cache* cache
  * The weights p * row are rounded to fp16 once, the largest 2^14: 2^-11 of each
  * down to 2^-28 of the largest, nothing below 2^-39 of it (for which a row below
  * 2^-90 counts as that).  The sum of the p takes every position, however far apart
- * the row scales lie; among positions that one warp takes (32 of each 128) beside one
- * whose scale is beyond 2^100, those of p above scale * 2^-140 of its p.
+ * the row scales lie; where the largest weight's scale is beyond 2^100, over the
+ * positions that one warp takes, to scale * 2^-140 of its p.
  * plan.ring_stages counts the units of 32 positions of one head in flight per CTA; a
  * CTA takes one KV head or two.  A V row with a scale of 2^120 or more, or a NaN, makes
  * the rows that attend it NaN (the append writes at most 2^117).

@@ -124,7 +124,9 @@ constexpr float kHugeScale = 0x1p120f;
 // A row's sum l carried to a larger maximum: l * 2^d, d <= 0, with alpha =
 // exp2(d).  With V scales that far apart (zero rows, whose p is up to 2^104, before
 // a row of 2^40) the factor alone is below fp32's range where the product is not:
-// then in two halves.
+// then in two halves.  (The 8-bit kernel adds it after the block: long step +0.9 %,
+// mix 0.4, head_dim 64 1.7, 16 query rows -3.  With the factors left to the branch of a
+// changed maximum, as for 4 bits, 0.2, 1.4, 1.7 and 0.5.)
 __device__ __forceinline__ float carry_sum(float l, float d, float alpha) {
   if (alpha != 0.f || l == 0.f) return l * alpha;
   const float h = fast_exp2(0.5f * d);
@@ -335,7 +337,7 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, floa
   }
   uint32_t pb_hi[2][NT8][2], pb_lo[2][NT8][2];
   bool rescale = false;
-  float alpha[NT8][2];
+  float alpha[NT8][2], l_old[NT8][2], m_old[NT8][2];
 #pragma unroll
   for (int j = 0; j < NT8; ++j) {
     float w[4][2];
@@ -365,6 +367,8 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, floa
         l += p;
         w[i][e] = in ? p * vs[i] : 0.f;
       }
+      l_old[j][e] = l_part[j][e];
+      m_old[j][e] = m_run[j][e];
       l_part[j][e] = l;
       m_run[j][e] = m_new;
     }
@@ -377,6 +381,14 @@ __device__ __forceinline__ void quant_block(uint8_t* kt, const float* ks_s, floa
     }
   }
   if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+    for (int j = 0; j < NT8; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (alpha[j][e] == 0.f && l_old[j][e] != 0.f) {  // as carry_sum
+          const float h = fast_exp2(0.5f * (m_old[j][e] - m_run[j][e]));
+          l_part[j][e] += l_old[j][e] * h * h;
+        }
 #pragma unroll
     for (int mi = 0; mi < D / 16; ++mi)
 #pragma unroll
@@ -749,18 +761,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
   if (threadIdx.x < R) {
     int hd;
     const int g = head_row(threadIdx.x, hd);
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; w += HC) M = fmaxf(M, ml_s[w + hd][g].x);
-    float L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w += HC) {
-      const float2 ml = ml_s[w + hd][g];
-      const float c = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
-      if (ml.y != 0.f) L += c * ml.y;
-      cw_s[w + hd][g] = c;
-    }
-    row_s[threadIdx.x] = make_float2(M, L);
+    row_s[threadIdx.x] = fold_states<kWarps, HC, GP>(ml_s, cw_s, hd, g);
   }
   named_barrier_sync(1, kWarps * 32);
   const bool dead = bad_s != 0 || abort_s != 0;
