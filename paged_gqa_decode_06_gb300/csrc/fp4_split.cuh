@@ -1051,7 +1051,7 @@ __global__ void __launch_bounds__(Fp4Cfg<D, NQ, HC>::kThreads, Fp4Cfg<D, NQ, HC>
 #pragma unroll
     for (int w = 0; w < kWarps; w += HC) {
       const float c = cw_s[w + hd][g];
-      if (c == 0.f) continue;
+      if (c < 0.f) continue;
       const float4 v =
           *reinterpret_cast<const float4*>(acc_s + ((w + hd) * GP + g) * kRowStride + 4 * q);
       O.x += c * v.x;

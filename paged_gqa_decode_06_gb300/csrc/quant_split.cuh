@@ -152,7 +152,8 @@ __device__ __forceinline__ float settle(float& m, float& l) {
 }
 
 // The state (m, l) of row g of head hd over the warps that have it, in fixed order, and
-// each warp's factor for its accumulators.
+// each warp's factor for its accumulators: -1 where it saw no position of the row (a
+// factor of 0 still carries a NaN).
 template <int kWarps, int HC, int GP>
 __device__ __forceinline__ float2 fold_states(const float2 (&ml_s)[kWarps][GP],
                                               float (&cw_s)[kWarps][GP], int hd, int g) {
@@ -168,7 +169,7 @@ __device__ __forceinline__ float2 fold_states(const float2 (&ml_s)[kWarps][GP],
   }
 #pragma unroll
   for (int w = 0; w < kWarps / HC; ++w) {
-    const float c = l[w] == 0.f ? 0.f : fast_exp2(m[w] - M);
+    const float c = l[w] == 0.f ? -1.f : fast_exp2(m[w] - M);
     if (l[w] != 0.f) L += c * l[w];
     cw_s[HC * w + hd][g] = c * f[w];
   }
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(QuantCfg<D, NT8, HC>::kThreads, QuantCfg<D, NT
 #pragma unroll
     for (int w = 0; w < kWarps; w += HC) {
       const float c = cw_s[w + hd][g];
-      if (c == 0.f) continue;
+      if (c < 0.f) continue;
       const float4 v =
           *reinterpret_cast<const float4*>(acc_s + ((w + hd) * GP + g) * kRowStride + 4 * q);
       O.x += c * v.x;
