@@ -563,8 +563,10 @@ int decode_kv_append_fp4(const decode_attn_params* p, const decode_kv_cache* cac
                          const int32_t* seq_lens, const int32_t* page_table, int32_t* err_flag,
                          void* stream);
 
-/* decode_kv_read of a DECODE_ATTN_KV_E2M1 cache: code * block * row, rounded
- * once. */
+/* decode_kv_read of a DECODE_ATTN_KV_E2M1 cache: code * block * row, rounded to
+ * the element type.  With finite scales a cell beyond its range reads as its largest
+ * number, so finite rows read back finite (a block's code 6 can stand for more than the
+ * largest value: of 65504, 67584). */
 int decode_kv_read_fp4(const decode_attn_params* p, const decode_kv_cache* cache,
                        int32_t total_rows, const int32_t* page_table, const int32_t* row_offsets,
                        const int32_t* starts, void* k_out, void* v_out, int32_t* err_flag,
@@ -583,7 +585,8 @@ int decode_kv_read_fp4(const decode_attn_params* p, const decode_kv_cache* cache
  * positions that one warp takes, to scale * 2^-140 of its p.
  * plan.ring_stages counts the units of 32 positions of one head in flight per CTA; a
  * CTA takes one KV head or two.  A V row with a scale of 2^120 or more, or a NaN, makes
- * the rows that attend it NaN (the append writes at most 2^117).
+ * the rows that attend it NaN (the append writes at most 2^117).  An output beyond the
+ * element type's range is an Inf.
  */
 int decode_attn_fp4_make_plan(const decode_attn_params* p, int32_t num_sms,
                               decode_attn_plan* plan);

@@ -362,8 +362,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_fp4_kernel(const ReadRows a)
         s[i] = __ldg(a.scales[i] + row);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    // kSat: a cell beyond the type's range is its largest number (a block's code 6 can
+    // stand for more than the value it came from: 65504 becomes 67584); not so under a
+    // row scale that is no finite number
+    auto put = [&](int i, auto sat) {
+      constexpr bool kSat = decltype(sat)::value;
       const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
       const uint32_t two = e4m3_to_half2(block[i]);
       const __half2 pair = *reinterpret_cast<const __half2*>(&two);
@@ -379,11 +382,19 @@ __global__ void __launch_bounds__(kThreads) kv_read_fp4_kernel(const ReadRows a)
           for (int j = 0; j < 4; ++j) {  // code * block is exact in fp16
             const float2 f =
                 __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h[j]), scale));
-            w[4 * k + j] = ElemOps<E>::pack2(f.x * s[i], f.y * s[i]);
+            w[4 * k + j] = kSat ? ElemOps<E>::pack2_sat(f.x * s[i], f.y * s[i])
+                                : ElemOps<E>::pack2(f.x * s[i], f.y * s[i]);
           }
         }
         store_32(a.out[i] + ((size_t)row0 * per_row + e) * 4 + 2 * b, w, a.wide);
       }
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (fabsf(s[i]) < INFINITY)
+        put(i, std::true_type{});
+      else
+        put(i, std::false_type{});
     }
   }
 }
