@@ -1035,6 +1035,27 @@ def _check_rope_table(table, head_dim: int, index: int):
         raise ValueError(f"table rotates {table.shape[1]} dims, the heads have {head_dim}")
 
 
+class _RopeGrad(torch.autograd.Function):
+    """decode_rope of rows that require a gradient: the rotation is linear, so that is
+    the rotation by the negative angle (and its own gradient this one again)."""
+
+    @staticmethod
+    def forward(ctx, x, positions, table, interleaved, backward, err_flag):
+        ctx.save_for_backward(positions, table)
+        ctx.interleaved, ctx.turned_back = interleaved, backward
+        return decode_rope(x, positions, table, interleaved, backward, None, err_flag)
+
+    @staticmethod
+    def backward(ctx, grad):
+        # (an expanded gradient, or one that lies off 16 bytes, is copied)
+        grad = grad.contiguous()
+        if grad.data_ptr() % 16:
+            grad = grad.clone()
+        positions, table = ctx.saved_tensors
+        x_grad = decode_rope(grad, positions, table, ctx.interleaved, not ctx.turned_back)
+        return x_grad, None, None, None, None, None
+
+
 def decode_rope(x, positions, table, interleaved: bool = False, backward: bool = False, out=None,
                 err_flag=None, stream=None):
     """Rows of heads x [rows, heads, head_dim] (fp16 or bf16; the rows may be
@@ -1043,8 +1064,9 @@ def decode_rope(x, positions, table, interleaved: bool = False, backward: bool =
     / 2) or with ``interleaved`` (2 i, 2 i + 1); the dims from rot_dim on stay.
     Returns ``out``, by default a new contiguous tensor; x itself is allowed.
     ``backward`` turns by the negative angle: the gradient with respect to x
-    from that with respect to out.  A position outside the table gives a zero
-    row."""
+    from that with respect to out, which autograd takes for an x that requires
+    one (``out`` cannot be given then; positions and table get none).  A position
+    outside the table gives a zero row."""
     quick = _quick_module if _quick_module is not _UNSET else _quick()
     if quick is not None:
         r = quick.rope(x, positions, table, interleaved, backward, out, err_flag, stream)
@@ -1054,6 +1076,11 @@ def decode_rope(x, positions, table, interleaved: bool = False, backward: bool =
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return decode_rope(x, positions, table, interleaved, backward, out, err_flag, stream)
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out cannot be given for an x that requires a gradient")
+        with torch.cuda.stream(stream):
+            return _RopeGrad.apply(x, positions, table, interleaved, backward, err_flag)
     et = _elem_dtype(x)
     x_stride = _row_stride(x, et, "x", index)
     rows, heads, D = x.shape

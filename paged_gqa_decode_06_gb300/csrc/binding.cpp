@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 
 #include "../../include/decode_attn.h"
 
@@ -211,7 +212,8 @@ PyObject* quick_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
   int64_t xs, os;
   const at::Tensor* x = half_type(type) ? rows_of(a[0], index, type, &xs) : nullptr;
-  if (!x) return other_way();
+  // (a gradient is the Python way's)
+  if (!x || (x->requires_grad() && c10::GradMode::is_enabled())) return other_way();
   const at::Tensor* pos = dense(a[1], index, at::kInt, {x->size(0)});
   const at::Tensor* table = dense(a[2], index, at::kFloat);
   bool interleaved, backward;
