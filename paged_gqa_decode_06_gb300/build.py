@@ -12,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,10 +31,11 @@ LIB_CHECKED_PATH = os.path.join(BUILD_CHECKED, LIB_CHECKED_NAME)
 
 def binding_path() -> str:
     """The Python binding's quick way (csrc/binding.cpp), one module for both builds.
-    It is compiled against one torch's classes, so its name carries the version:
-    another torch does not load it."""
+    It is compiled against one torch's classes and one Python's objects, so its name
+    carries both: another does not load it."""
     import torch
-    return os.path.join(BUILD, f"_binding-{torch.__version__}.so")
+    return os.path.join(BUILD, f"_binding-{torch.__version__}"
+                               f"{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
 
 
 def checked_requested() -> bool:
@@ -84,7 +86,6 @@ def build_binding(force: bool = False):
     src = os.path.join(CSRC, "binding.cpp")
     header = os.path.join(os.path.dirname(HERE), "include", "decode_attn.h")
     try:
-        import sysconfig
         import torch
         from torch.utils.cpp_extension import include_paths, library_paths
     except ImportError:
