@@ -93,22 +93,27 @@ def build_binding(force: bool = False):
     path = binding_path()
     if not force and _up_to_date(path, [src, header]):
         return path
-    os.makedirs(BUILD, exist_ok=True)
     tmp = path + f".tmp{os.getpid()}"
     abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
            *["-I" + p for p in [*include_paths(), sysconfig.get_paths()["include"]]], src, "-o",
            tmp, *["-L" + p for p in library_paths()], "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    error = ""
     try:
+        os.makedirs(BUILD, exist_ok=True)
+        if os.path.exists(path):  # (of other sources: not loaded if this build fails)
+            os.remove(path)
         r = subprocess.run(cmd, capture_output=True, text=True)
-        error = r.stderr if r.returncode else ""
+        if r.returncode:
+            error = r.stderr
+        else:
+            os.replace(tmp, path)
     except OSError as e:
         error = str(e)
     if error:
         warnings.warn(f"the quick binding was not built, calls take the Python way:\n{error}")
         return None
-    os.replace(tmp, path)
     return path
 
 
@@ -125,8 +130,9 @@ def build(force: bool = False, verbose: bool = False, checked=None) -> str:
         return lib
     srcs = _sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        ex.submit(build_binding, force)
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(lambda s: _compile(s, out_dir, extra), srcs))
+        binding.result()  # (raises what it raised)
     if verbose:
         for _, log in results:
             print(log)
