@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
                                    a.Hkv + h) * (D / 2) + c / 2;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t w = __ldg(v + i);
+            const uint32_t w = v[i];  // (not the read-only path: an append may just have run)
             const float2 f = ElemOps<E>::unpack2(w & wild2<E>(w));
             o[2 * i] += f.x;
             o[2 * i + 1] += f.y;

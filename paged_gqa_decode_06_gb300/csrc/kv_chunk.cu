@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_rows_kernel(const KvRows a) 
       for (int i = 0; i < 2; ++i) {
         x[u][i] = __ldcs(static_cast<const Raw*>(a.src[i]) + cell);
         if constexpr (kQuant)
-          s[u][i] = __ldg(a.scales[i] +
-                          ((size_t)at.x * a.Hkv + (c >> a.head_shift)) * a.page_size + at.y);
+          // (not the read-only path: an append before may still run when this starts)
+          s[u][i] = a.scales[i][((size_t)at.x * a.Hkv + (c >> a.head_shift)) * a.page_size + at.y];
       }
     }
 #pragma unroll

@@ -358,8 +358,10 @@ __global__ void __launch_bounds__(kThreads) kv_read_fp4_kernel(const ReadRows a)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         q[i] = __ldcs(a.codes[i] + cell);
-        block[i] = __ldg(a.blocks[i] + (row << a.unit_shift) + u);
-        s[i] = __ldg(a.scales[i] + row);
+        // (not the read-only path: the kernel before, which an append may be, can still
+        // run when this one starts)
+        block[i] = a.blocks[i][(row << a.unit_shift) + u];
+        s[i] = a.scales[i][row];
       }
     }
     // kSat: a cell beyond the type's range is its largest number (a block's code 6 can

@@ -65,7 +65,7 @@ __device__ __forceinline__ int2 place_row_alone(const RowMap& a, int row, bool* 
   int lo = -1, hi = a.B;  // the largest b with offsets[b] <= row
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(a.offsets + mid) <= row)
+    if (ld_global_s32(a.offsets + mid) <= row)
       lo = mid;
     else
       hi = mid;

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeRows a) {
     x[1][0] = __ldcs(src + per_head + item.x);
     x[1][1] = __ldcs(src + per_head + item.y);
   }
-  const int pos = __ldg(a.positions + row);
+  const int pos = ld_global_s32(a.positions + row);
   if (pos < 0 || pos >= a.rope.rows) {
     if (h == 0 && unit == 0) raise_error(a.err, DECODE_ATTN_DEV_BAD_LEN);
     x[0][0] = x[0][1] = x[1][0] = x[1][1] = make_uint4(0u, 0u, 0u, 0u);

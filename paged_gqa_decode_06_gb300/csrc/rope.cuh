@@ -35,7 +35,8 @@ __device__ __forceinline__ void rope_load(RopePairs& p, const RopeArgs& r, int p
   const float4* c = reinterpret_cast<const float4*>(r.table + (size_t)pos * r.rot + 8 * unit);
   const float4* s = reinterpret_cast<const float4*>(r.table + (size_t)pos * r.rot + r.rot / 2 +
                                                     8 * unit);
-  const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
+  // (not the read-only path: what wrote the table may still run when this kernel starts)
+  const float4 c0 = c[0], c1 = c[1], s0 = s[0], s1 = s[1];
   // (the sign as bits: a negation of each sine)
   const uint32_t flip = r.backward ? 0x80000000u : 0u;
   auto turn = [&](float x) { return __uint_as_float(__float_as_uint(x) ^ flip); };
