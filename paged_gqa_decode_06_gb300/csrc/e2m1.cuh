@@ -12,6 +12,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "e4m3.cuh"
 #include "elem.cuh"
 
@@ -64,6 +66,18 @@ __device__ __forceinline__ uint32_t e2m1_pack8(const float (&x)[8]) {
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
       : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// Two values to 16 bits, what is beyond the type's range as its largest number (a NaN
+// stays).
+template <class E>
+__device__ __forceinline__ uint32_t pack2_sat(float lo, float hi) {
+  uint32_t r;
+  if constexpr (std::is_same<E, __half>::value)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

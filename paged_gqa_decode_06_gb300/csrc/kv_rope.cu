@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_fp4_kernel(const ReadRows a)
           for (int j = 0; j < 4; ++j) {  // code * block is exact in fp16
             const float2 f =
                 __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h[j]), scale));
-            w[4 * k + j] = kSat ? ElemOps<E>::pack2_sat(f.x * s[i], f.y * s[i])
-                                : ElemOps<E>::pack2(f.x * s[i], f.y * s[i]);
+            w[4 * k + j] = kSat ? pack2_sat<E>(f.x * s[i], f.y * s[i])
+                            : ElemOps<E>::pack2(f.x * s[i], f.y * s[i]);
           }
         }
         store_32(a.out[i] + ((size_t)row0 * per_row + e) * 4 + 2 * b, w, a.wide);
