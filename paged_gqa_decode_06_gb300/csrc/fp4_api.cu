@@ -14,14 +14,21 @@ namespace {
 constexpr int kDefaultSplitMin = 256;
 constexpr int kLargeChunkCap = 2048;
 constexpr int64_t kPairBytes = 32 << 20;
+// Up to four sequences take one head a CTA and few_shards; more, two heads and pieces of
+// 1.7 waves.  Of lengths all alike the first way is quicker to eight (32/8 heads of 128,
+// 65536 positions: 4 sequences 67 us and 83, 6 96 and 114, 8 123 and 132); of U[1, L] the
+// second is from five on (64/8 of 131072: 4 sequences 92 and 114, 5 114 and 100, 8 216 and
+// 153), and the lengths are not known here.
 constexpr int kFewSequences = 4;
 constexpr double kSmallStep = 1280 * 1024;   // bytes per SM
 constexpr double kSmallPiece = 96 * 1024;    // bytes per CTA slot
 constexpr double kSmRingBytes = 152 * 1024;  // in flight per SM
 // Of a few long sequences: what an SM takes for a position of one head with 1, 2, 3
 // or 4 CTAs at once (ns at head_dim 128, up to 4 query rows; 8 rows take 1.15 times
-// as long), and what the merge takes per shard and query row (one sequence of
-// 131072 positions by 38, 57 and 76 shards 45, 42 and 42 us).
+// as long; other head_dims by their size and 16 rows as 8, which is no measurement: four
+// sequences of 32768 take 68 us so with 16 rows and 65 at head_dim 256, by pieces 74 and
+// 75), and what the merge takes per shard and query row (one sequence of 131072 positions
+// by 38, 57 and 76 shards 45, 42 and 42 us).
 constexpr double kRowNs[4] = {5.7, 4.6, 4.1, 3.95};
 constexpr double kMergeNs = 20;
 

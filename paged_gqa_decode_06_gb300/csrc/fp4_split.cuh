@@ -32,20 +32,23 @@
 //    of a score lie two lanes apart; of the lanes that add them up one half takes
 //    the unit's first 16 positions on and the other the last 16.
 //  * The weights are rounded to fp16 once, the largest 2^14: 11 bits down to 2^-28
-//    of it, nothing below 2^-39.  (A second product for the remainder would move
-//    the result by less than its own rounding, and takes the products that the
-//    parities need.)
+//    of it, nothing below 2^-39; the sum keeps them unrounded.  Against 64 bits an
+//    fp16 result is off by 2.1e-4 to 2.5e-4 (rel. L2), by its own rounding alone 2.1e-4,
+//    a bf16 one by its rounding.  (The 8-bit kernel's second product for the remainder
+//    takes the products that the parities need here.)
 //  * A block without a number among its scales (NaN) is the only way that codes
 //    reach a product as no number, so a position outside a row's range is
 //    cleared by its V blocks' scales alone.
 //
-// Measured (GB300): four sequences of 131072 positions, 64 heads over 8, 133 us (4.8
-// TB/s; the 8-bit cache 187), 64 of U[1, 8192] with 32 heads 83.5 us (3.9 TB/s; 109),
-// 64 of 8192 128 us, one of 3060 8.6 us.  Instructions bound it: 340 for 16 positions of a
-// head (64 conversions, 64 scalings, 24 products, 60 for the copies, 70 for the
-// softmax), issued in 60 % of the slots that 16 warps an SM have; the ALU is busy
-// 45 % of the time, the tensor cores 34 %, DRAM 60 %.  With the copies left out the long
-// step takes 113 us, without the softmax 116, without either product 111.
+// Measured (GB300): four sequences of 131072 positions, 64 heads over 8, 132.5 us (4.8
+// TB/s; the 8-bit cache 187), 64 of U[1, 8192] with 32 heads 84 us (3.9 TB/s; 111),
+// 64 of 8192 128.5 us, one of 3060 8.7 us; 16 of 8192 with 16 rows a head 69 us (2.3 TB/s).
+// No unit is at its limit in the long step: 340 instructions for 16 positions of a head (64
+// conversions, 64 scalings, 24 products, 60 for the copies, 70 for the softmax) take 60 %
+// of the slots that 16 warps an SM have; the ALU is busy 44 % of the time, the tensor
+// cores 34 %, DRAM 60 %.  With the copies left out it takes 113 us, without the softmax
+// 116, without either product 111.  Uneven lengths are short of balance beside that: 64
+// of 8192 reach 4960 GB/s, of U[1, 8192] 3860.
 #pragma once
 
 #include "e2m1.cuh"

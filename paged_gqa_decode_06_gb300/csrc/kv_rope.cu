@@ -17,12 +17,13 @@
 // those of decode_rope followed by an append of its result.
 //
 // Measured (GB300): called run after run, 32,354 rows of 8 heads of 128, rotated, with 32
-// query heads, into 8 bits 120.5 us (6.1 TB/s); 30011 rows of 8 heads of 64 as 16 bits 25
+// query heads, into 8 bits 120.4 us (6.1 TB/s); 30011 rows of 8 heads of 64 as 16 bits 25
 // us (5.2 TB/s: K and V are a fifth of the rows they are sliced from).  Replayed in one
-// graph, 32,354 rows into 4 bits 49 us (3.5 TB/s: 20 instructions a value, the ALU 57 %
-// busy, first of them the divisions, two operations each); 71,533 rows back from 4 bits 64
-// us (5.9 TB/s; with 16-byte stores and 16 values a thread a fourth more); one row each
-// of 64 3.5 us, the launch.
+// graph, 32,354 rows into 4 bits 48.6 us (3.5 TB/s: 20 instructions a value, first of them
+// the divisions, two operations each; 68 % of the issue slots, the ALU 57 % busy, so neither
+// is at its limit, nor is DRAM); 71,533 rows back from 4 bits 64 us (5.9 TB/s; with 16-byte
+// stores and 16 values a thread a fourth more); one row each of 64 sequences 3.5 us, the
+// launch and two round trips.
 #include <algorithm>
 
 #include "chunk_launch.h"
@@ -36,7 +37,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 64;   // rows of a block, a thread each to place them
-constexpr int kBlocksPerSm = 8;  // that a call is cut into, at least, where it has the rows
+constexpr int kBlocksPerSm = 8;  // that a call is cut into, where it has the rows
 
 struct AppendRows : RowMap {
   RopeArgs rope;
@@ -402,9 +403,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_fp4_kernel(const ReadRows a)
 }
 
 // Rows per block: finding the rows' places is most of a small block's time, so a call
-// is cut into two waves of blocks and no more (30011 rows of 8 heads of 64: 25.6 us,
-// in blocks of 8 rows 30; 32,354 rows into 8 bits, with queries, 120.7 and 119.5; 5000
-// of those without queries 13.2 and 14.2).
+// is cut into about 8 blocks an SM of up to 64 rows each, and into more blocks only
+// beyond that (30011 rows of 8 heads of 64, 25 rows a block: 25 us, in blocks of 8 rows
+// 30; 32,354 rows into 8 bits, with queries, 120.4 and 118.6; 5000 of those without
+// queries 13.2 and 14.2).  Four blocks of the append are on an SM at once, six of the
+// read.
 template <class Kernel, class Args>
 int launch_rows(Kernel kern, Args& a, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};

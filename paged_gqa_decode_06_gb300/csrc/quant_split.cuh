@@ -29,7 +29,7 @@
 //    weights of a context far below one token's would end at 2^-25).
 //
 // Measured (GB300): four sequences of 131072 positions, 64 heads over 8, 187 us
-// (5.9 TB/s; 195 run after run), 64 of U[1, 8192] 109 us, one of 3060 9.1 us.  The
+// (5.9 TB/s; 195 run after run), 64 of U[1, 8192] 111 us, one of 3060 9.5 us.  The
 // copies bound it: with consumers that only release the stages the long step
 // takes 170 to 185 us, since a head's row is one 128-byte line of the eight that
 // lie together.
