@@ -1041,9 +1041,16 @@ class _RopeGrad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, positions, table, interleaved, backward, err_flag):
-        ctx.save_for_backward(positions, table)
+        out = decode_rope(x, positions, table, interleaved, backward, None, err_flag)
+        # (saving notices a change of either until the gradient is taken; those made in
+        # inference mode cannot be saved, nor have they versions to look at)
+        ctx.held = None
+        if positions.is_inference() or table.is_inference():
+            ctx.held = positions, table
+        else:
+            ctx.save_for_backward(positions, table)
         ctx.interleaved, ctx.turned_back = interleaved, backward
-        return decode_rope(x, positions, table, interleaved, backward, None, err_flag)
+        return out
 
     @staticmethod
     def backward(ctx, grad):
@@ -1051,7 +1058,7 @@ class _RopeGrad(torch.autograd.Function):
         grad = grad.contiguous()
         if grad.data_ptr() % 16:
             grad = grad.clone()
-        positions, table = ctx.saved_tensors
+        positions, table = ctx.held or ctx.saved_tensors
         x_grad = decode_rope(grad, positions, table, ctx.interleaved, not ctx.turned_back)
         return x_grad, None, None, None, None, None
 

@@ -98,6 +98,10 @@ def test_what_a_gradient_refuses_and_what_it_leaves_alone(pkg):  # noqa: F811
     for out in (leaf, torch.empty_like(leaf)):
         with pytest.raises(ValueError, match="out"):
             pkg.decode_rope(leaf, *a, out=out)
+    for bad, exc in ((dict(positions=None), TypeError), (dict(positions=a[0].long()), TypeError),
+                     (dict(table=a[1][0]), ValueError), (dict(positions=a[0][:2]), ValueError)):
+        with pytest.raises(exc):
+            pkg.decode_rope(leaf, **{**dict(positions=a[0], table=a[1]), **bad})
     plain = pkg.decode_rope(x.to(DEV), *a)
     for off in (torch.no_grad, torch.inference_mode):
         with off():
@@ -111,6 +115,13 @@ def test_what_a_gradient_refuses_and_what_it_leaves_alone(pkg):  # noqa: F811
     t.mul_(2)
     with pytest.raises(RuntimeError, match="modified by an inplace"):
         y.sum().backward()
+    # a table and positions made where nothing is recorded
+    with torch.inference_mode():
+        made_there = (pos.to(DEV), table.to(DEV))
+    leaf.grad = None
+    pkg.decode_rope(leaf, *made_there).sum().backward()
+    one = rotate(torch.ones(6, 3, 64), pos, table, backward=True).half()
+    assert torch.equal(leaf.grad.cpu(), one)
     # a position outside the table: a zero row, and no gradient through it
     p = a[0].clone()
     p[2] = 10 ** 6
