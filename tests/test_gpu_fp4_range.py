@@ -47,3 +47,31 @@ def test_fp4_v_scales_far_apart(pkg, Hq, Hkv, D, large, kw):  # noqa: F811
         # a step of that, 2^-17, where a weight is taken and where it is carried on
         w = weight(d) + 2.0 ** -16
         assert_rows(got, ref, mass + least_weights(d) / (2 * w), BF16, w, exponent)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,window", [(1, 8, 2, 128, 0), (2, 8, 2, 64, 0),
+                                               (3, 4, 2, 128, 0), (3, 5, 1, 128, 300)])
+def test_fp4_v_scales_far_apart_in_large_steps(pkg, T, Hq, Hkv, D, window):  # noqa: F811
+    """The same with two KV heads per CTA and with several tokens: zero rows and rows of
+    2^60 to 2^110 mixed over positions and heads."""
+    cap = 131072 // 16 * 8
+    d = cache(901, [900, 1, 0, 77, 2300, 64], T, Hq=Hq, Hkv=Hkv, D=D, PS=16, dtype=BF16,
+              max_pages=cap, loud=False)
+    if Hkv == 2:
+        p = pkg.DecodeAttnParams(6, Hq, Hkv, D, 16, cap, d["cache"][0].shape[0], 0, 1.0, window,
+                                 0, 0, 0, T, 1, 0)
+        plan = pkg.decode_attn_fp4_make_plan(p, 152)
+        assert (plan.grid_x if plan.head_fastest else plan.grid_y) == 1
+    g = torch.Generator().manual_seed(902)
+    shape = d["cache"][3].shape
+    kinds = torch.tensor([0.0, 0.0, 2.0 ** 70, 2.0 ** 120])
+    for per_page in (False, True):  # rows of one page alike, or each its own
+        n = shape[:2] + (1,) if per_page else shape
+        e = dict(d, cache=list(d["cache"]))
+        e["cache"][3] = d["cache"][3] * kinds[torch.randint(0, 4, n, generator=g)]
+        ref, mass = reference(e, window)
+        w = weight(e) + 2.0 ** -16
+        for kw in ({}, dict(force_chunk=256, schedule=1)):
+            got, err = run(pkg, e, T, window, **kw)
+            assert err == 0
+            assert_rows(got, ref, mass + least_weights(e, window) / (2 * w), BF16, w)
